@@ -140,6 +140,11 @@ __device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+__device__ __forceinline__ uint32_t h2_min(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -523,16 +528,18 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
       };
       const int row_at = g * (KT * 128) + token * 128, flip = (token % 8) * 16;
       auto put_k = [&]() {
-        float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pairs[0]));
-        f.x = fminf(f.x, 8188.f);              // 8 s stays a binary16 number
-        const uint32_t s2 = pack_f16(f.x, f.x);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pairs[0]));
+        // The high part's scale is at most 8188, so that 8 of it stay a binary16 number; what a larger one (up to 8736)
+        // has beyond it is the remainder's: with the high part a multiple of 4, c s less it is one below 4400, 11 bits.
+        const float top = fminf(f.x, 8188.f);
+        const uint32_t s2 = pack_f16(f.x, f.x), top2 = pack_f16(top, top);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           uint32_t c[4], hi4[4], lo4[4];
           codes8<8>(word(0, i), c);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            hi4[e] = h2_mul(c[e], s2);
+            hi4[e] = h2_mul(c[e], top2);
             lo4[e] = h2_fma(c[e], s2, hi4[e] ^ 0x80008000u);                // the product's exact remainder
           }
           uint8_t* to = sk + row_at + ((i * 16) ^ flip);
@@ -547,18 +554,25 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
         fence_proxy_async_smem();
       };
       auto put_v = [&](uint8_t* stage) {
-        uint32_t p = pairs[1];
-        // at the end of binary16's range: z + 15 s may not round past it
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
-        if (fmaf(15.f, f.x, f.y) > 65504.f)
-          p = (p & 0xffff0000u) | __half_as_ushort(__float2half_rz((65504.f - f.y) * (1.f / 15.f)));
-        const uint32_t s2 = __byte_perm(p, p, 0x1010), z2 = __byte_perm(p, p, 0x3232);
+        const uint32_t p = pairs[1], s2 = __byte_perm(p, p, 0x1010), z2 = __byte_perm(p, p, 0x3232);
+        uint8_t* to = stage + row_at;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           uint32_t c[4];
           codes8<0>(word(1, i), c);
-          *reinterpret_cast<uint4*>(stage + row_at + ((i * 16) ^ flip)) =
+          *reinterpret_cast<uint4*>(to + ((i * 16) ^ flip)) =
               make_uint4(h2_fma(c[0], s2, z2), h2_fma(c[1], s2, z2), h2_fma(c[2], s2, z2), h2_fma(c[3], s2, z2));
+        }
+        // z + 15 s may pass binary16's end (by 60, less than 2^-10 of it): its largest number then, in place of infinity
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
+        if (fmaf(15.f, f.x, f.y) >= 65520.f) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            uint4* at = reinterpret_cast<uint4*>(to + ((i * 16) ^ flip));
+            const uint4 v = *at;
+            constexpr uint32_t kEnd = 0x7bff7bffu;         // 65504
+            *at = make_uint4(h2_min(v.x, kEnd), h2_min(v.y, kEnd), h2_min(v.z, kEnd), h2_min(v.w, kEnd));
+          }
         }
         fence_proxy_async_smem();
       };

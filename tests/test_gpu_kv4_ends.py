@@ -1,0 +1,78 @@
+"""GPU parity of the paged 4-bit cache at the ends of what it may hold."""
+
+import numpy as np
+import pytest
+
+from oracle import kv4 as o
+from tests.test_gpu_kv4 import attention_tolerance, dev
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+
+@pytest.fixture(scope="module")
+def tq():
+    from kv_cache_vector_15_b200 import tq as _tq
+    return _tq
+
+
+def filled(tq, rng, lens, k, v, ps):
+    """A cache that holds the rows k, v (one sequence after the other) on pages
+    in random order, and its table."""
+    H, d = k.shape[1:]
+    need = [-(-n // ps) for n in lens]
+    perm = rng.permutation(sum(need) + 1).astype(np.int32)
+    table = np.zeros((len(lens), max(need)), np.int32)
+    at, slots = 0, []
+    for i, n in enumerate(lens):
+        table[i, :need[i]] = perm[at:at + need[i]]
+        at += need[i]
+        slots.append(table[i, np.arange(n) // ps].astype(np.int64) * ps + np.arange(n) % ps)
+    C = tq.KV4Cache.empty(sum(need) + 1, H, d, ps)
+    C.append(dev(k), dev(v), dev(np.concatenate(slots)))
+    C.check()
+    return C, dev(table)
+
+
+def compare(tq, C, table, lens, nq, q, causal=True, window=0, max_q=None):
+    """The call against the oracle: NaN where the oracle has NaN, the rest within the derived bounds."""
+    cu = np.concatenate([[0], np.cumsum(nq)]).astype(np.int32)
+    hint = max_q or max(nq)
+    out, lse = C.attention(q, table, dev(np.array(lens, np.int32)), dev(cu), hint, causal=causal, window=window, return_lse=True)
+    C.check()
+    dtype, d = "bf16" if q.dtype == torch.bfloat16 else "f32", q.shape[2]
+    many = dtype == "bf16" and hint * q.shape[1] // C.kv_heads > 16
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref = o.attention(q.double().cpu().numpy(), C.pool.cpu().numpy(), table.cpu().numpy(), lens, cu, C.kv_heads, C.page_size,
+                          d ** -0.5, causal, window)
+        tol, ltol = attention_tolerance(ref, max(lens), dtype, many, d)
+    got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    nan, lnan = np.isnan(ref[0]), np.isnan(ref[1])
+    assert np.array_equal(np.isnan(got), nan), (np.isnan(got).sum(), nan.sum())
+    assert np.array_equal(np.isnan(gl), lnan)
+    inf = np.isneginf(ref[1])
+    assert np.array_equal(np.isneginf(gl), inf)
+    off = np.abs(got - ref[0])[~nan] / tol[~nan]
+    assert off.size == 0 or off.max() <= 1, off.max()
+    loff = (np.abs(gl - ref[1]) / ltol)[~(lnan | inf)]
+    assert loff.size == 0 or loff.max() <= 1, loff.max()
+    return nan, lnan
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("nq,dtype", [(1, "bf16"), (3, "f32"), (40, "bf16")])
+def test_groups_that_span_the_whole_range(tq, d, nq, dtype):
+    """Groups from -65504 to 65504 (scales of 8736, codes times scale past
+    binary16's end): every kernel reads the values that the codes stand for.
+    Spans on both sides of 8 s = 65504 and of z + 15 s = 65504."""
+    rng = np.random.default_rng(d + nq)
+    n, H = 90, 2
+    x = np.linspace(-65504, 65504, 64)[None, None, None].repeat(2 * n * H * (d // 64), 0).reshape(2, n, H, d // 64, 64)
+    x = rng.permuted(x, axis=-1) * np.where(rng.random((2, n, H, d // 64, 1)) < 0.5, 1.0, rng.uniform(0.9, 1, (2, n, H, d // 64, 1)))
+    k, v = x.reshape(2, n, H, d).astype(np.float32)
+    C, table = filled(tq, rng, [n], k, v, 16)
+    q = dev((rng.standard_normal((nq, 2 * H, d)) * 2e-5 * (128 / d) ** 0.5).astype(np.float32)).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    for causal in (True, False):
+        nan, _ = compare(tq, C, table, [n], [nq], q, causal)
+        assert not nan.any()
