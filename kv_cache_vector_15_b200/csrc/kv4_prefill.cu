@@ -220,6 +220,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
     mbar_init(drain, 1);
     mbar_fence_init();
   }
+  // Tensor memory is taken behind the wait: a kernel before this one that has let its dependents start may itself still
+  // want some, and would get none from a CTA that holds all of it and waits for that kernel's end.
+  wait_for_stream();
   if (warp == Z::kSoft + Z::kUnpack) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
@@ -229,7 +232,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  wait_for_stream();
   const Part part = part_of<KT, kCost>(P, worker, R, 1);
   int32_t* desc = P.desc + worker * kDescInts;
   if (threadIdx.x == 0) desc[0] = 0;

@@ -9,7 +9,10 @@ namespace tq {
 
 // A kernel launched by launch_dependent may be set up while the kernel before
 // it in the stream ends.  It calls this first, in every thread: what that
-// kernel wrote is visible afterwards, and what it read may be written.  (An
+// kernel wrote is visible afterwards, and what it read may be written.  Before
+// the call a kernel may set up its own shared memory and barriers, and nothing
+// else: what it took there and another kernel waits for (tensor memory) would
+// be held until that other one has ended.  (An
 // earlier set-up yet, by an explicit trigger behind this, measured no difference.)
 __device__ __forceinline__ void wait_for_stream() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
