@@ -176,7 +176,9 @@ struct Shape {
   static constexpr int kQx = 128 * 32, kKx = KT * 32;    // the 16 more terms
   static constexpr int kAtQx = QT * kQ + 4 * kKV;        // behind Q, K high, K low, V, V
   static constexpr int kBars = kAtQx + QT * kQx + kKx;   // barriers behind the operands
+  static constexpr int kLost = CH * KT / 32;             // words of a stage's marks of NaN values: a bit per group and token
   static constexpr int kBytes = kBars + 256 + 1024;      // and slack for the 1024-byte alignment
+  static_assert(144 + 2 * kLost * 4 <= 256, "the marks fit behind the barriers");
   static constexpr int kSmem = kBytes < 120 * 1024 ? 120 * 1024 : kBytes;   // one CTA per SM: it takes all of TMEM
   static constexpr int kSoft = 4 * QT;                   // softmax warps
   static constexpr int kUnpack = KT * CH / 32;           // unpacking warps: a thread per token and 64 coordinates
@@ -199,6 +201,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
   uint64_t *q_full = bars, *s_full = bars + 2, *p_full = bars + 4, *o_done = bars + 6, *k_full = bars + 8,
            *k_free = bars + 10, *v_full = bars + 12, *v_free = bars + 14, *drain = bars + 16;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+  uint32_t* lost = reinterpret_cast<uint32_t*>(bars + 18);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int worker = blockIdx.x;
 
@@ -349,6 +352,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
         const uint32_t t_s = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + qt * KT;
         const uint32_t t_o = tmem + (static_cast<uint32_t>((warp % 4) * 32) << 16) + Z::kO + qt * D;
         float m = kLowest, l = 0.f;
+        uint32_t lost_groups = 0;              // in which the row sees a NaN value
         for (int i = 0; i < n_tiles; ++i) {
           const uint32_t n = q_tiles_done[qt] + i;
           if (!(ok = wait_warp(s_full + qt, n))) break;
@@ -444,6 +448,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
           tc_fence_before();
+          // NaN values are zero in V (a weight of zero times NaN would reach the rows that do not see them): the rows that
+          // see one look for its mark.  The products wait for V as well, so this wait costs nothing; the marks stand until
+          // these weights have been used.
+          const uint32_t tile = tiles_done + i;
+          if (!(ok = wait_warp(v_full + (tile & 1u), tile >> 1))) break;
+          const uint32_t* marks = lost + (tile & 1u) * Z::kLost;
+          uint32_t any = 0;
+#pragma unroll
+          for (int k = 0; k < Z::kLost; ++k) any |= marks[k];
+          if (any != 0) {
+#pragma unroll 1
+            for (int k = 0; k < Z::kLost; ++k) {
+              const int first = key0 + k % (KT / 32) * 32, a = max(lo - first, 0), b = min(hi - first, 31);
+              if (a <= b && (marks[k] & (0xffffffffu << a) & (0xffffffffu >> (31 - b))) != 0) lost_groups |= 1u << (k / (KT / 32));
+            }
+          }
           mbar_arrive(p_full + qt);
         }
         if (n_tiles > 0 && ok) {
@@ -457,6 +477,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
           __nv_bfloat16* out = static_cast<__nv_bfloat16*>(P.out) + orow * D;
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
+            const float by = (lost_groups >> (c / 64)) & 1u ? __int_as_float(0x7fffffff) : inv;
             uint32_t v[32];
             if (n_tiles > 0) {
               tmem_ld32(t_o + c, v);
@@ -469,7 +490,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
             for (int e = 0; e < 32; e += 8) {  // columns 0 1 2 3 ... hold coordinates 0 4 1 5 2 6 3 7 of each 8
               float o[8];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) o[(k & 1) * 4 + k / 2] = __uint_as_float(v[e + k]) * inv;
+              for (int k = 0; k < 8; ++k) o[(k & 1) * 4 + k / 2] = __uint_as_float(v[e + k]) * by;
               if (whole) {
                 if (live)
                   *reinterpret_cast<uint4*>(out + c + e) =
@@ -555,9 +576,15 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
         *reinterpret_cast<uint16_t*>(skx + at_more(token, 3 * g + 2)) = static_cast<uint16_t>(hl & 0xffffu);
         fence_proxy_async_smem();
       };
-      auto put_v = [&](uint8_t* stage) {
-        const uint32_t p = pairs[1], s2 = __byte_perm(p, p, 0x1010), z2 = __byte_perm(p, p, 0x3232);
-        uint8_t* to = stage + row_at;
+      auto put_v = [&](uint32_t st) {
+        uint32_t p = pairs[1];
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
+        const bool nan = f.x != f.x || f.y != f.y;
+        const uint32_t nans = __ballot_sync(0xffffffffu, nan);
+        if (lane == 0) lost[st * Z::kLost + g * (KT / 32) + token / 32] = nans;
+        if (nan) p = 0;
+        const uint32_t s2 = __byte_perm(p, p, 0x1010), z2 = __byte_perm(p, p, 0x3232);
+        uint8_t* to = sv + st * Z::kKV + row_at;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           uint32_t c[4];
@@ -566,7 +593,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
               make_uint4(h2_fma(c[0], s2, z2), h2_fma(c[1], s2, z2), h2_fma(c[2], s2, z2), h2_fma(c[3], s2, z2));
         }
         // z + 15 s may pass binary16's end (by 60, less than 2^-10 of it): its largest number then, in place of infinity
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p));
         if (fmaf(15.f, f.x, f.y) >= 65520.f) {
 #pragma unroll 1
           for (int i = 0; i < 8; ++i) {
@@ -598,7 +624,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) k_kv4_prefill(const __g
           id = page_of(t0 + i + 2);
         }
         if (!(ok = wait_warp(v_free + st, (n >> 1) ^ 1u))) break;
-        put_v(sv + st * Z::kKV);
+        put_v(st);
         mbar_arrive(v_full + st);
         if (next) fetch(1, blk);
       }

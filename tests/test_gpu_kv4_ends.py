@@ -35,6 +35,15 @@ def filled(tq, rng, lens, k, v, ps):
     return C, dev(table)
 
 
+def spoil(C, table, seq, part, tokens, head, group):
+    """NaN pairs for a group of a head's rows, written by hand (part 0: K, 1: V)."""
+    nb, d = C.page_size // 16, C.d
+    for t in tokens:
+        page, at = int(table[seq, t // C.page_size]), t % C.page_size
+        pair = (head * nb + at // 16) * 18 * d + part * 9 * d + 8 * d + at % 16 * (d // 16) + 4 * group
+        C.pool[page, pair:pair + 4] = torch.tensor([0xff, 0x7f] * 2, dtype=torch.uint8, device="cuda")
+
+
 def compare(tq, C, table, lens, nq, q, causal=True, window=0, max_q=None):
     """The call against the oracle: NaN where the oracle has NaN, the rest within the derived bounds."""
     cu = np.concatenate([[0], np.cumsum(nq)]).astype(np.int32)
@@ -76,3 +85,35 @@ def test_groups_that_span_the_whole_range(tq, d, nq, dtype):
     for causal in (True, False):
         nan, _ = compare(tq, C, table, [n], [nq], q, causal)
         assert not nan.any()
+
+
+def cache_with_nan(tq, rng, d, dtype, lens, nq, where):
+    """Two kv heads of random rows, NaN pairs in head 0 of the first sequence:
+    a key three quarters through the new tokens, values before, among and behind them."""
+    H, g, n0 = 2, 2, lens[0]
+    k, v = rng.standard_normal((2, sum(lens), H, d)).astype(np.float32)
+    C, table = filled(tq, rng, lens, k, v, 32)
+    if where != "v":
+        spoil(C, table, 0, 0, [n0 - nq[0] + nq[0] * 3 // 4], 0, d // 64 - 1)
+    if where != "k":
+        for t in (n0 - 1, n0 - nq[0] + nq[0] // 2, n0 - nq[0] - 10, 3):
+            spoil(C, table, 0, 1, [t], 0, int(rng.integers(0, d // 64)))
+    q = dev((1.5 * rng.standard_normal((sum(nq), H * g, d))).astype(np.float32)).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    return C, table, q
+
+
+@pytest.mark.parametrize("d,dtype,lens,nq,window", [
+    (128, "bf16", [40, 130], [1, 1], 0), (128, "bf16", [130, 40], [4, 3], 0), (64, "f32", [130, 40], [4, 3], 0),
+    (256, "f32", [130, 40], [7, 3], 5), (128, "bf16", [300, 77], [60, 40], 0), (128, "bf16", [300, 77], [60, 40], 40),
+    (64, "bf16", [300, 77], [60, 40], 40), (256, "bf16", [300, 77], [60, 40], 40), (128, "bf16", [3000, 77], [200, 1], 700),
+    (256, "bf16", [3000, 77], [200, 1], 0)])
+@pytest.mark.parametrize("where", ["k", "v", "both"])
+def test_nan_in_the_cache_reaches_the_rows_that_see_it(tq, d, dtype, lens, nq, window, where):
+    """And no others: a key's NaN all of a row's outputs, a value's NaN the
+    coordinates of its group; rows whose mask leaves the token out, other heads
+    and other sequences do not change."""
+    C, table, q = cache_with_nan(tq, np.random.default_rng(sum(lens) + d + window), d, dtype, lens, nq, where)
+    nan, _ = compare(tq, C, table, lens, nq, q, True, window)
+    assert nan.any() and not nan.all()
+    nan, _ = compare(tq, C, table, lens, nq, q, False)
+    assert nan.any() and not nan.all()
