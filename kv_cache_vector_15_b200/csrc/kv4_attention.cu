@@ -79,6 +79,11 @@ __host__ __device__ constexpr int stages_of(int d, int nt) {
 constexpr int tiles_for(int d, int64_t rows) { return d == 256 || rows <= 4 ? 1 : 2; }
 __host__ __device__ constexpr int ctas_of(int d, int nt) { return d <= 128 ? (nt == 1 ? 3 : 2) : 2; }
 
+__device__ __forceinline__ float max_nan(float a, float b) {   // NaN where one is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 __device__ __forceinline__ float from_bits_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float from_bits_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 __device__ __forceinline__ void mma_u8s8(int (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -447,6 +452,9 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT))
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             sc[bk][t][k] = ex2(y[bk][t][k]);
+            // at an edge a weight of zero stands for a token that is not seen: a seen one's is not less than 2^-126 (a
+            // part of 2^-118 of the sum at most), so that a NaN value behind it counts here as it does elsewhere
+            if (kEdge && y[bk][t][k] != -INFINITY) sc[bk][t][k] = max_nan(sc[bk][t][k], 1.17549435e-38f);
             den[t][k & 1] += sc[bk][t][k];
           }
 

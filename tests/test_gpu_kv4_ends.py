@@ -117,3 +117,20 @@ def test_nan_in_the_cache_reaches_the_rows_that_see_it(tq, d, dtype, lens, nq, w
     assert nan.any() and not nan.all()
     nan, _ = compare(tq, C, table, lens, nq, q, False)
     assert nan.any() and not nan.all()
+
+
+def test_nan_behind_a_weight_that_is_zero_in_fp32(tq):
+    """A NaN value counts however small its token's weight is, inside a run of keys and at its edge."""
+    rng = np.random.default_rng(8)
+    for n, nq, dtype in ((41, 1, "bf16"), (64, 1, "bf16"), (77, 4, "f32"), (300, 20, "bf16")):
+        k, v = rng.standard_normal((2, n, 1, 64)).astype(np.float32)
+        k[:, :, 0] = 8.0
+        for t in (2, n - 1):
+            low = k.copy()
+            low[t, 0, 0] = -8.0
+            C, table = filled(tq, rng, [n], low, v, 16)
+            spoil(C, table, 0, 1, [t], 0, 0)
+            q = torch.zeros((nq, 2, 64), device="cuda", dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+            q[:, :, 0] = 300.0
+            nan, lnan = compare(tq, C, table, [n], [nq], q, causal=False)
+            assert nan.all() and not lnan.any()
