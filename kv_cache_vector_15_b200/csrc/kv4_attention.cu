@@ -270,7 +270,8 @@ __global__ void __launch_bounds__(kWarps * 32, ctas_of(D, NT))
       int ex = 0;
       frexpf(top, &ex);
       ex = top > 0.f ? min((kF32 ? 29 : 21) - ex, 120) : 0;
-      const float up = pow2(ex), down = P.scale_log2 * pow2(-ex);
+      // an infinite coordinate: its logits are infinite or NaN, and NaN the softmax of such (a NaN comes in by the sums)
+      const float up = pow2(ex), down = top < INFINITY ? P.scale_log2 * pow2(-ex) : __int_as_float(0x7fffffff);
 #pragma unroll
       for (int g = 0; g < G; ++g) {
         float sum = 0.f;

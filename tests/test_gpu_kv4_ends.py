@@ -134,3 +134,18 @@ def test_nan_behind_a_weight_that_is_zero_in_fp32(tq):
             q[:, :, 0] = 300.0
             nan, lnan = compare(tq, C, table, [n], [nq], q, causal=False)
             assert nan.all() and not lnan.any()
+
+
+@pytest.mark.parametrize("nq,dtype", [(1, "bf16"), (3, "f32"), (40, "bf16")])
+@pytest.mark.parametrize("what", [np.nan, np.inf, -np.inf])
+def test_rows_of_queries_that_are_not_finite(tq, nq, dtype, what):
+    """A query with a NaN or an infinity gives NaN (its logits are infinite or
+    NaN), also where all of its logits are -infinity; the rows beside it stay as they are."""
+    rng = np.random.default_rng(nq)
+    lens, H, g, d = [77, 90], 2, 3, 64
+    k, v = (rng.standard_normal((2, sum(lens), H, d)) + 9.0).astype(np.float32)      # every key is positive
+    C, table = filled(tq, rng, lens, k, v, 16)
+    q = rng.standard_normal((2 * nq, H * g, d)).astype(np.float32)
+    q[nq - 1, 1, 7], q[nq, 4, 0] = what, what
+    nan, lnan = compare(tq, C, table, lens, [nq, nq], dev(q).to(torch.bfloat16 if dtype == "bf16" else torch.float32), False)
+    assert nan.all(-1).sum() == 2 and lnan.sum() == 2
