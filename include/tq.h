@@ -347,7 +347,8 @@ tq_status tq_qk_norm_rope(const void* q, int64_t ld_q, int q_heads, const void* 
  *   z = f16(min x),  s = f16(f32(max(max x - z, 0) / 15)),  code = clamp(rint((x - z) / s), 0, 15)
  *
  * with the exact quotient, ties to the even code (s = 0: code 0); |x| beyond
- * 65504 is taken as 65504.
+ * 65504 is taken as 65504.  A group with a NaN in it is NaN: its pair is two
+ * binary16 NaNs (0x7fff), its codes are 0, and all 64 coordinates read as NaN.
  *
  * pool: device bytes [n_pages][kv_heads][page_size / 16] blocks; a block holds
  * 16 consecutive tokens of one kv head in 18 d bytes:
@@ -409,6 +410,9 @@ size_t tq_kv4_attention_workspace_bytes(tq_kv4 cache, tq_dtype dtype, int q_head
  *   them (decoder tokens against an encoder's states), and window must be 0.
  *   A token that sees nothing gets out = 0 and lse = -infinity.  Tokens of no
  *   sequence (behind cu_q[n_seqs]) keep what out and lse held.
+ *   NaN: a key's reaches all outputs of the rows that see its token, a value's
+ *   the 64 coordinates of its group of these, however small the weight; a query
+ *   row with a NaN or an infinity gives NaN.  No other row changes.
  *   max_q: the largest number of new tokens of a sequence, used to choose the
  *   kernel (results hold for any value >= 1).
  * Query rows are taken to 2^-21 of their largest coordinate (fp32 rows: 2^-29),

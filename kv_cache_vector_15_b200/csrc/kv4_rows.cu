@@ -84,6 +84,18 @@ __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const fl
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The smaller, the larger; NaN where one is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // What the host works out once per call.
 struct Sizes {
   int64_t n_slots;                     // of the pool
@@ -149,20 +161,21 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 5) k_kv4_append
     float lo = q[0], hi = q[0];
 #pragma unroll
     for (int i = 1; i < 16; ++i) {
-      lo = fminf(lo, q[i]);
-      hi = fmaxf(hi, q[i]);
+      lo = min_nan(lo, q[i]);
+      hi = max_nan(hi, q[i]);
     }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
     }
-    // coordinates past the range get the codes of its ends, as the ends themselves would
-    lo = fminf(fmaxf(lo, -65504.f), 65504.f);
-    hi = fminf(fmaxf(hi, -65504.f), 65504.f);
+    // coordinates past the range get the codes of its ends, as the ends themselves would; a NaN makes scale and zero NaN
+    // (no quotient is formed then: the codes are 0)
+    lo = min_nan(max_nan(lo, -65504.f), 65504.f);
+    hi = min_nan(max_nan(hi, -65504.f), 65504.f);
     const __half zh = __float2half_rn(lo + 0.f);           // + 0: a zero has one form
     const float zero = __half2float(zh), span = __fsub_rn(hi, zero);
-    const __half sh = __float2half_rn(span > 0.f ? __fdiv_rn(span, 15.f) : 0.f);
+    const __half sh = __float2half_rn(__fdiv_rn(max_nan(span, 0.f), 15.f));
     const float s = __half2float(sh);
     const float inv = s > 0.f ? __frcp_rn(15.f * s) : 0.f;
     constexpr float kRound = 12582912.f;                   // 1.5 * 2^23

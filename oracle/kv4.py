@@ -17,12 +17,15 @@ BLOCK = 16
 # ------------------------------------------------------------- the format --
 
 def quantize(x):
-    """Rows [..., d] to (codes int [..., d], scale f16 [..., d / 64], zero f16 [..., d / 64])."""
+    """Rows [..., d] to (codes int [..., d], scale f16 [..., d / 64], zero f16
+    [..., d / 64]); a group with a NaN: codes 0, scale and zero the NaN 0x7fff."""
     x = np.clip(np.asarray(x, np.float32), -65504, 65504)
     g = x.reshape(*x.shape[:-1], x.shape[-1] // GROUP, GROUP)
     zero = (g.min(-1) + np.float32(0)).astype(np.float16)
     span = (g.max(-1) - zero.astype(np.float32)).astype(np.float32)
     scale = (np.where(span > 0, span, np.float32(0)) / np.float32(15)).astype(np.float32).astype(np.float16)
+    for pair in (scale, zero):
+        pair.view(np.uint16)[np.isnan(g).any(-1)] = 0x7fff
     s, z = scale.astype(np.float64)[..., None], zero.astype(np.float64)[..., None]
     with np.errstate(divide="ignore", invalid="ignore"):
         t = np.where(s > 0, (g.astype(np.float64) - z) / s, 0.0)

@@ -149,3 +149,37 @@ def test_rows_of_queries_that_are_not_finite(tq, nq, dtype, what):
     q[nq - 1, 1, 7], q[nq, 4, 0] = what, what
     nan, lnan = compare(tq, C, table, lens, [nq, nq], dev(q).to(torch.bfloat16 if dtype == "bf16" else torch.float32), False)
     assert nan.all(-1).sum() == 2 and lnan.sum() == 2
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_nan_rows_stay_nan(tq, dtype):
+    """A NaN coordinate makes its group of 64 NaN: codes 0 with a pair of NaN;
+    other groups, rows and heads are what they were without it."""
+    rng = np.random.default_rng(3)
+    n, H, d, ps = 40, 3, 128, 16
+    x = rng.standard_normal((n, H, d)).astype(np.float32)
+    clean = x.copy()
+    x[4, 1, 70] = np.nan
+    x[5, 2, :64] = np.nan
+    x[6, 0, 3], x[6, 0, 4] = np.nan, np.inf
+    x[7, 0, [64, 127]] = [-np.inf, np.nan]
+    x[8, 1, ::64] = -np.nan
+    bad = np.isnan(x).reshape(n, H, 2, 64).any(-1)
+    tt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    C = tq.KV4Cache.empty(4, H, d, ps)
+    slots = dev(rng.permutation(4 * ps)[:n].astype(np.int64))
+    kv, vv = C.append(dev(x).to(tt), dev(clean).to(tt), slots, return_values=True)
+    _, plain = C.append(dev(clean).to(tt), dev(x).to(tt), slots, return_values=True)      # over the rows before
+    C.check()
+    spread = np.repeat(bad, 64, -1)
+    assert np.array_equal(torch.isnan(kv).cpu().numpy(), spread) and np.array_equal(torch.isnan(plain).cpu().numpy(), spread)
+    assert torch.equal(kv[dev(~spread)], vv[dev(~spread)]) and not torch.isnan(vv).any()
+    kk, vb = C.dequant(slots, out_dtype=tt)
+    assert torch.equal(kk, vv) and np.array_equal(torch.isnan(vb).cpu().numpy(), spread)
+    want = np.zeros(tuple(C.pool.shape), np.uint8)
+    for part, y in ((0, clean), (1, x)):
+        c, s, z = o.quantize(dev(y).to(tt).float().cpu().numpy())
+        for t in range(n):
+            for h in range(H):
+                o.write_slot(want, int(slots[t]), part, h, c[t, h], s[t, h], z[t, h], H, d, ps)
+    assert np.array_equal(C.pool.cpu().numpy(), want)
