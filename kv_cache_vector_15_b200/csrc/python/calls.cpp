@@ -408,22 +408,26 @@ PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// pool, pairs, n_pages, stream
+// pool, pairs, n_pages, n_layers, stream
 PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    count(n_args, 4);
+    count(n_args, 5);
     const at::Tensor pool = tensor(a[0], "pool"), pairs = tensor(a[1], "pairs");
-    const int64_t n_pages = integer(a[2]);
-    Place at(a[3]);
+    const int64_t n_pages = integer(a[2]), asked = a[3] == Py_None ? -1 : integer(a[3]);
+    Place at(a[4]);
     at.all(pool, pairs);
     if (pairs.dim() != 2) throw ValueError("pairs must be contiguous int32 [n, 2]");
     want(pairs, at::kInt, {pairs.size(0), 2}, "pairs");
     if (!pool.is_contiguous()) throw ValueError("pool must be contiguous");
     if (n_pages < 1) throw ValueError("n_pages must be >= 1");
-    int64_t layers = 0;
-    if (pool.dim() >= 1 && pool.size(0) == n_pages && (pool.dim() < 3 || pool.size(1) != n_pages)) layers = 1;
-    else if (pool.dim() >= 2 && pool.size(1) == n_pages) layers = pool.size(0);
-    else throw ValueError("pool must be [" + std::to_string(n_pages) + ", ...] or [n_layers, " + std::to_string(n_pages) + ", ...]");
+    if (a[3] != Py_None && asked < 1) throw ValueError("n_layers must be >= 1");
+    const bool one = pool.dim() >= 1 && pool.size(0) == n_pages && asked <= 1;
+    const bool many = pool.dim() >= 2 && pool.size(1) == n_pages && (asked < 0 || pool.size(0) == asked);
+    if (asked < 0 && one && many && pool.dim() >= 3 && n_pages > 1)
+      throw ValueError("pool is one layer of pages or " + std::to_string(n_pages) + " layers of them: n_layers has to say which");
+    if (!one && !many)
+      throw ValueError("pool must be [" + std::to_string(n_pages) + ", ...] or [n_layers, " + std::to_string(n_pages) + ", ...]");
+    const int64_t layers = one ? 1 : pool.size(0);
     std::optional<NoGil> free(std::in_place);
     const int64_t stride = static_cast<int64_t>(pool.nbytes()) / std::max<int64_t>(1, layers);
     const tq_status st = tqlib.pages_copy(ptr(pool), layers, stride, stride / n_pages, n_pages, ids(pairs), pairs.size(0), at.stream);

@@ -599,16 +599,18 @@ class PageMoves:
     pairs: "object"
     n_pages: int
 
-    def copy(self, pool, stream=None):
-        """Copy the pages of ``pool``: a contiguous tensor [n_pages, ...] or [n_layers, n_pages, ...]."""
-        copy_pages(pool, self.pairs, self.n_pages, stream)
+    def copy(self, pool, stream=None, n_layers=None):
+        """Copy the pages of ``pool``: a contiguous tensor [n_pages, ...] or [n_layers, n_pages, ...] (see copy_pages)."""
+        copy_pages(pool, self.pairs, self.n_pages, stream, n_layers)
 
 
-def copy_pages(pool, pairs, n_pages: int, stream=None):
+def copy_pages(pool, pairs, n_pages: int, stream=None, n_layers: int | None = None):
     """Copy page pairs[i, 0] to page pairs[i, 1] of ``pool``, a contiguous
     tensor [n_pages, ...] or [n_layers, n_pages, ...] (a cache's pool, or one
-    field of a packed cache with its rows grouped by pages)."""
-    (_calls or _load_calls()).copy_pages(pool, pairs, n_pages, stream)
+    field of a packed cache with its rows grouped by pages).  ``n_layers`` says
+    which (1: the first); it is needed where a shape of three or more dimensions
+    reads both ways, [n_pages, n_pages, ...].  [n_pages, n_pages] is one layer."""
+    (_calls or _load_calls()).copy_pages(pool, pairs, n_pages, n_layers, stream)
 
 
 class PageTable:

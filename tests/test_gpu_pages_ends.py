@@ -1,0 +1,72 @@
+"""Calls of the page table that have to be refused, or done whole: bad entries in
+rows, no room for slots, tables of another device, layouts that read two ways."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a CUDA device")]
+
+
+@pytest.fixture(scope="module")
+def tq():
+    from kv_cache_vector_15_b200 import tq as _tq
+    return _tq
+
+
+def i32(x):
+    return torch.tensor(list(x), dtype=torch.int32, device="cuda")
+
+
+def arrays(T):
+    return [x.clone() for x in (T.table, T.lens, T.refs)]
+
+
+def other(tq, T):
+    return tq.PageTable(torch.full_like(T.table, 77), torch.full_like(T.lens, 78), torch.full_like(T.refs, 79), T.page_size)
+
+
+def unchanged(tq, T, before, out, call):
+    """The call is recorded as a bad one and leaves in's contents in out."""
+    r = call()
+    with pytest.raises(tq.TQError) as e:
+        T.check()
+    assert e.value.status == tq.TQ_ERR_INVALID_ARG
+    assert all(torch.equal(x, y) for x, y in zip(before, arrays(T)))
+    if out is not None:
+        assert all(torch.equal(x, y) for x, y in zip(before, arrays(out)))
+    return r
+
+
+@pytest.mark.parametrize("n,m", [(8, 4), (5, 9)])
+def test_pools_that_read_two_ways(tq, n, m):
+    """[n, n, m] is one layer of n pages or n layers of n pages: the call asks which."""
+    pool = torch.arange(n * n * m, device="cuda", dtype=torch.int32).view(n, n, m)
+    pairs = i32([1, 0, 2, n - 1, -1, -1]).view(3, 2)
+    keep = pool.clone()
+    with pytest.raises(ValueError, match="n_layers"):
+        tq.copy_pages(pool, pairs, n)
+    with pytest.raises(ValueError, match="n_layers"):
+        tq.PageMoves(pairs, n).copy(pool)
+    assert torch.equal(pool, keep)
+    one, all_of = keep.clone(), keep.clone()
+    one[0], one[n - 1] = keep[1], keep[2]
+    all_of[:, 0], all_of[:, n - 1] = keep[:, 1], keep[:, 2]
+    a, b = pool.clone(), pool.clone()
+    tq.copy_pages(a, pairs, n, n_layers=1)
+    tq.PageMoves(pairs, n).copy(b, n_layers=n)
+    assert torch.equal(a, one) and torch.equal(b, all_of)
+    tq.copy_pages(a.view(1, n, n, m), pairs, n)                  # one reading: layers first
+    tq.copy_pages(b[0], pairs, n)
+    tq.copy_pages(pool.view(n, n * m), pairs, n)
+    assert torch.equal(pool, one)
+    with pytest.raises(ValueError):
+        tq.copy_pages(pool, pairs, n, n_layers=2)
+    with pytest.raises(ValueError):
+        tq.copy_pages(pool, pairs, n + 1, n_layers=1)
+    with pytest.raises(ValueError):
+        tq.copy_pages(pool.view(n * n, m), pairs, n, n_layers=n)
+    tq.copy_pages(torch.zeros((1, 1, 4), device="cuda"), i32([0, 0]).view(1, 2), 1)      # one page: both readings are one
+    with pytest.raises(ValueError):
+        tq.copy_pages(pool, pairs, n, n_layers=0)
