@@ -333,14 +333,15 @@ PyObject* pages_extend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     at.on(given);
     if (n_slots < 0) throw ValueError("n_slots must be >= 0");
     std::optional<NoGil> free(std::in_place);
-    at::Tensor slots = at.output(make(table, {n_slots}, at::kLong));
+    // a list of no slots has an address too: without one the call would take it that no list is wanted
+    at::Tensor slots = at.output(make(table, {std::max<int64_t>(1, n_slots)}, at::kLong));
     size_t bytes = 0;
     const at::Tensor ws = workspace(given, tqlib.pages_workspace_bytes(in, n), table, &bytes);
     const tq_status st = tqlib.pages_extend(in, out, n, ids(seqs), ids(more), static_cast<int64_t*>(ptr(slots)), n_slots, ptr(ws), bytes,
                              at.stream);
     free.reset();
     check(st, "tq_pages_extend");
-    return THPVariable_Wrap(slots);
+    return THPVariable_Wrap(n_slots ? slots : slots.narrow(0, 0, 0));
   });
 }
 

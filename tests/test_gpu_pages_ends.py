@@ -70,3 +70,16 @@ def test_pools_that_read_two_ways(tq, n, m):
     tq.copy_pages(torch.zeros((1, 1, 4), device="cuda"), i32([0, 0]).view(1, 2), 1)      # one page: both readings are one
     with pytest.raises(ValueError):
         tq.copy_pages(pool, pairs, n, n_layers=0)
+
+
+def test_no_room_for_slots_is_no_room(tq):
+    """n_slots = 0 is a list of no slots, not a call without a list."""
+    T = tq.PageTable.empty(4, 4, 10, 16)
+    T.extend(i32([0]), i32([20]), 20)
+    T.check()
+    before = arrays(T)
+    s = unchanged(tq, T, before, None, lambda: T.extend(i32([3]), i32([5]), 0))
+    assert s.shape == (0,) and s.dtype == torch.int64
+    unchanged(tq, T, before, None, lambda: T.extend(i32([3, 0]), i32([0, 1]), 0))
+    T.extend(i32([3, 0]), i32([0, 0]), 0)
+    T.check()
