@@ -439,7 +439,10 @@ tq_status tq_kv4_attention(tq_kv4 cache, const void* q, tq_dtype dtype, int64_t 
  * which has the same sizes and is either the same three arrays (in place) or
  * three others (all of them then written whole; `in` stays).  A call does all
  * of its work or none of it: where an index is out of range, a row is too
- * short or too few pages are free, out takes in's contents unchanged and
+ * short, a row that it goes by (a fork's sources, the sequences that end, all
+ * rows in a compaction, an extended sequence's partly filled page) holds an
+ * entry that is no page or a free one, or too few pages are free, out takes
+ * in's contents unchanged and
  * status records why (tq_cache_status).  Free pages are given out in order of
  * their index, so results do not depend on timing.
  *   sizes: n_seqs in [1, 2^20], max_pages >= 1, n_pages in [1, 2^30],

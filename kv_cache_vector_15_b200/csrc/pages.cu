@@ -1,10 +1,11 @@
 // The page table of a cache: growth, forks, ends, compaction, and the copies
 // of pages that these ask for.
 //
-// Each table call is two kernels.  The plan (one CTA, the other CTAs of its
-// grid copy `in` to `out` where these differ) checks every index and finds the
+// Each table call is two kernels.  The plan (one CTA; the other CTAs of its
+// grid check the entries of the rows that the call goes by, and copy `in` to
+// `out` where these differ) checks every index and finds the
 // free pages in order of their index; the second kernel takes a row of the
-// table per CTA, and leaves all as it was if the plan failed.  Ranks come from
+// table per CTA, and leaves all as it was if a check failed.  Ranks come from
 // ballots and a scan over the CTA's warps, not from atomics, so pages are
 // given out in the same order every time.  Bound: launch latency and one pass
 // over refs (up to 16384 pages per step of the plan's CTA); the copies are bound by
@@ -24,14 +25,19 @@ constexpr int kPlan = 1024;                    // threads of a planning CTA
 constexpr int kSub = 16;                       // pages per lane and step of a pass over refs
 constexpr int kRowThreads = 128;
 
+constexpr int kOthers = 147;                   // CTAs behind the planning one, at most
+
 // Workspace (int32 words): [0] failed, [1] used pages, [2] tokens of an
-// extension; then map [n_seqs], three arrays [n], and list [n_pages].
+// extension, from [8] on a word per checking CTA, not 0 where it met a bad
+// row; then map [n_seqs], three arrays [n], and list [n_pages].
+constexpr int kHead = 160;
+static_assert(8 + kOthers <= kHead && kOthers <= 2 * kRowThreads, "a word per checking CTA; a row's CTA reads them in two steps");
 struct Ws {
   int32_t *head, *map, *len, *off, *tok, *list;
 };
 __host__ __device__ __forceinline__ Ws ws_of(void* ws, int64_t n_seqs, int64_t n) {
-  int32_t* p = static_cast<int32_t*>(ws);
-  return {p, p + 8, p + 8 + n_seqs, p + 8 + n_seqs + n, p + 8 + n_seqs + 2 * n, p + 8 + n_seqs + 3 * n};
+  int32_t *p = static_cast<int32_t*>(ws), *a = p + kHead + n_seqs;
+  return {p, p + kHead, a, a + n, a + 2 * n, a + 3 * n};
 }
 
 // Exclusive sum over the CTA of one value per thread, and the total.
@@ -106,11 +112,52 @@ __device__ __forceinline__ void record(int32_t* status, int32_t bits) {
 
 // refs and lens of `in` to `out`, by the CTAs behind the planning one.
 __device__ __forceinline__ void copy_state(const tq_pages& in, const tq_pages& out, bool refs) {
+  if (in.table == out.table) return;
   const int64_t at = static_cast<int64_t>(blockIdx.x - 1) * blockDim.x + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x - 1) * blockDim.x;
   for (int64_t i = at; i < in.n_seqs; i += step) out.lens[i] = in.lens[i];
   if (refs)
     for (int64_t i = at; i < in.n_pages; i += step) out.refs[i] = in.refs[i];
+}
+
+// The rows of sequences list[0..n) (no list: of all), by the CTAs behind the
+// planning one, a warp per row: every entry that the length covers is a page
+// that somebody owns.
+__device__ __forceinline__ void check_rows(const tq_pages& in, const int32_t* list, int64_t n, const Ws& w) {
+  constexpr int kEach = 8;                     // entries of a lane in flight
+  const int others = gridDim.x - 1, lane = threadIdx.x % 32;
+  int bad = 0;
+  for (int64_t i = static_cast<int64_t>(threadIdx.x / 32) * others + blockIdx.x - 1; i < n; i += 32 * others) {
+    const int64_t s = list ? list[i] : i;
+    if (s < 0 || s >= in.n_seqs) continue;     // the plan's own check
+    const int64_t len = in.lens[s];
+    const int64_t pages = len <= 0 ? 0 : min((len + in.page_size - 1) / in.page_size, in.max_pages);
+    const int32_t* row = in.table + s * in.max_pages;
+    for (int64_t j0 = lane; j0 < pages; j0 += 32 * kEach) {
+      int32_t page[kEach];
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) page[k] = j0 + 32 * k < pages ? row[j0 + 32 * k] : row[j0];
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) bad |= page[k] < 0 || page[k] >= in.n_pages || in.refs[page[k]] <= 0;
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (threadIdx.x == 0) {
+    w.head[8 + blockIdx.x - 1] = bad;
+    if (bad) record(in.status, kStatusPages);
+  }
+}
+// Whether one of `checkers` CTAs met a bad row; called by a whole CTA.
+__device__ __forceinline__ bool rows_bad(const Ws& w, int checkers) {
+  int bad = 0;
+  for (int i = threadIdx.x; i < checkers; i += kRowThreads) bad |= w.head[8 + i];
+  return __syncthreads_or(bad) != 0;
+}
+// No moves, where a call is not done after all.
+__device__ __forceinline__ void no_moves(int32_t* moves, int64_t n) {
+  for (int64_t k = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x; k < 2 * n;
+       k += static_cast<int64_t>(gridDim.x) * kRowThreads)
+    moves[k] = -1;
 }
 
 __device__ __forceinline__ void clear_map(const Ws& w, int64_t n_seqs) {
@@ -121,9 +168,12 @@ __device__ __forceinline__ void clear_map(const Ws& w, int64_t n_seqs) {
 __global__ void __launch_bounds__(kPlan) k_plan_fork(tq_pages in, tq_pages out, int n, const int32_t* src,
                                                      const int32_t* dst, int32_t* moves, void* ws) {
   wait_for_stream();
-  if (blockIdx.x > 0) return copy_state(in, out, true);
-  __shared__ int sums[32];
   const Ws w = ws_of(ws, in.n_seqs, n);
+  if (blockIdx.x > 0) {
+    copy_state(in, out, true);
+    return check_rows(in, src, n, w);
+  }
+  __shared__ int sums[32];
   clear_map(w, in.n_seqs);
   __syncthreads();
   const int64_t cap = in.max_pages * in.page_size;
@@ -177,10 +227,11 @@ __global__ void __launch_bounds__(kPlan) k_plan_fork(tq_pages in, tq_pages out, 
 }
 
 __global__ void __launch_bounds__(kRowThreads) k_apply_fork(tq_pages in, tq_pages out, int n, const int32_t* src,
-                                                            bool same, void* ws) {
+                                                            int32_t* moves, int checkers, bool same, void* ws) {
   wait_for_stream();
   const Ws w = ws_of(ws, in.n_seqs, n);
-  const bool fail = w.head[0] != 0;
+  const bool bad = rows_bad(w, checkers), fail = bad || w.head[0] != 0;
+  if (bad) no_moves(moves, n);
   for (int64_t s = blockIdx.x; s < in.n_seqs; s += gridDim.x) {
     const int i = fail ? -1 : w.map[s];
     int32_t* to = out.table + s * in.max_pages;
@@ -195,8 +246,7 @@ __global__ void __launch_bounds__(kRowThreads) k_apply_fork(tq_pages in, tq_page
       int32_t page = -1;
       if (j < full) {
         page = from[j];
-        if (page >= 0 && page < in.n_pages) atomicAdd(out.refs + page, 1);
-        else record(in.status, kStatusPages);
+        atomicAdd(out.refs + page, 1);
       } else if (j == full && rank >= 0) {
         page = w.list[rank];
         out.refs[page] = 1;
@@ -313,8 +363,11 @@ __global__ void __launch_bounds__(kRowThreads) k_apply_extend(tq_pages in, tq_pa
 
 __global__ void __launch_bounds__(kPlan) k_plan_free(tq_pages in, tq_pages out, int n, const int32_t* seqs, void* ws) {
   wait_for_stream();
-  if (blockIdx.x > 0) return copy_state(in, out, true);
   const Ws w = ws_of(ws, in.n_seqs, n);
+  if (blockIdx.x > 0) {
+    copy_state(in, out, true);
+    return check_rows(in, seqs, n, w);
+  }
   clear_map(w, in.n_seqs);
   __syncthreads();
   int bad = 0;
@@ -330,10 +383,11 @@ __global__ void __launch_bounds__(kPlan) k_plan_free(tq_pages in, tq_pages out, 
   }
 }
 
-__global__ void __launch_bounds__(kRowThreads) k_apply_free(tq_pages in, tq_pages out, int n, bool same, void* ws) {
+__global__ void __launch_bounds__(kRowThreads) k_apply_free(tq_pages in, tq_pages out, int n, int checkers,
+                                                            bool same, void* ws) {
   wait_for_stream();
   const Ws w = ws_of(ws, in.n_seqs, n);
-  const bool fail = w.head[0] != 0;
+  const bool fail = rows_bad(w, checkers) || w.head[0] != 0;
   for (int64_t s = blockIdx.x; s < in.n_seqs; s += gridDim.x) {
     const bool ends = !fail && w.map[s] == 1;
     const int32_t* from = in.table + s * in.max_pages;
@@ -344,10 +398,7 @@ __global__ void __launch_bounds__(kRowThreads) k_apply_free(tq_pages in, tq_page
     if (!ends && same) continue;
     for (int64_t j = threadIdx.x; j < in.max_pages; j += kRowThreads) {
       const int32_t page = from[j];
-      if (ends && j < pages) {
-        if (page >= 0 && page < in.n_pages) atomicSub(out.refs + page, 1);
-        else record(in.status, kStatusPages);
-      }
+      if (ends && j < pages) atomicSub(out.refs + page, 1);
       to[j] = ends ? -1 : page;
     }
     if (ends && threadIdx.x == 0) out.lens[s] = 0;
@@ -357,9 +408,12 @@ __global__ void __launch_bounds__(kRowThreads) k_apply_free(tq_pages in, tq_page
 __global__ void __launch_bounds__(kPlan) k_plan_compact(tq_pages in, tq_pages out, int32_t* moves, int64_t most,
                                                         void* ws) {
   wait_for_stream();
-  if (blockIdx.x > 0) return copy_state(in, out, false);
-  __shared__ int sums[32];
   const Ws w = ws_of(ws, in.n_seqs, 0);
+  if (blockIdx.x > 0) {
+    copy_state(in, out, false);
+    return check_rows(in, nullptr, in.n_seqs, w);
+  }
+  __shared__ int sums[32];
   const int n_pages = static_cast<int>(in.n_pages), all = n_pages + 1;     // at most 2^30
   const int used = over_pages(in.refs, n_pages, all, sums, [](int, bool, int, int) {});
   // the k-th free place before `used` and the k-th used page from there on
@@ -387,13 +441,23 @@ __global__ void __launch_bounds__(kPlan) k_plan_compact(tq_pages in, tq_pages ou
   }
 }
 
-__global__ void __launch_bounds__(kRowThreads) k_apply_compact(tq_pages in, tq_pages out, const int32_t* moves,
-                                                               bool same, void* ws) {
+__global__ void __launch_bounds__(kRowThreads) k_apply_compact(tq_pages in, tq_pages out, int32_t* moves, int64_t most,
+                                                               int checkers, bool same, void* ws) {
   wait_for_stream();
   const Ws w = ws_of(ws, in.n_seqs, 0);
+  const bool bad = rows_bad(w, checkers);
   const int64_t count = w.head[0], used = w.head[1];
   const int64_t at = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kRowThreads;
+  if (bad) {                                   // out takes in's contents
+    no_moves(moves, most);
+    if (same) return;
+    for (int64_t p = at; p < in.n_pages; p += step) out.refs[p] = in.refs[p];
+    for (int64_t s = blockIdx.x; s < in.n_seqs; s += gridDim.x)
+      for (int64_t j = threadIdx.x; j < in.max_pages; j += kRowThreads)
+        out.table[s * in.max_pages + j] = in.table[s * in.max_pages + j];
+    return;
+  }
   // a pair's two counts belong to one thread, so working in place is safe
   for (int64_t k = at; k < count; k += step) {
     const int32_t high = moves[2 * k], hole = moves[2 * k + 1];
@@ -413,8 +477,7 @@ __global__ void __launch_bounds__(kRowThreads) k_apply_compact(tq_pages in, tq_p
       int32_t page = -1;
       if (j < pages) {
         page = in.table[s * in.max_pages + j];
-        if (page < 0 || page >= in.n_pages) record(in.status, kStatusPages);
-        else if (page >= used) page = w.list[page];
+        if (page >= used) page = w.list[page];
       }
       out.table[s * in.max_pages + j] = page;
     }
@@ -472,16 +535,17 @@ __global__ void __launch_bounds__(kCopyThreads) k_copy_pages(uint8_t* base, int6
 }
 
 dim3 rows_grid(const tq_pages& p) { return dim3(static_cast<unsigned>(std::min<int64_t>(p.n_seqs, 148 * 16))); }
-// the planning CTA, and the ones that copy where in and out differ
-dim3 plan_grid(const tq_pages& p, bool same) {
-  return dim3(same ? 1 : 1 + static_cast<unsigned>(std::min<int64_t>(147, (p.n_seqs + p.n_pages + kPlan - 1) / kPlan)));
+// the planning CTA, and the ones that check `rows` rows, and copy where in and out differ
+dim3 plan_grid(const tq_pages& p, bool same, int64_t rows) {
+  const int64_t copies = same ? 0 : (p.n_seqs + p.n_pages + kPlan - 1) / kPlan;
+  return dim3(1 + static_cast<unsigned>(std::min<int64_t>(kOthers, std::max(rows, copies))));
 }
 bool is_same(const tq_pages& a, const tq_pages& b) { return a.table == b.table; }
 
 }  // namespace
 
 size_t pages_ws_bytes(const tq_pages& p, int64_t n) {
-  return round16(static_cast<size_t>(8 + p.n_seqs + 3 * n + p.n_pages) * 4);
+  return round16(static_cast<size_t>(kHead + p.n_seqs + 3 * n + p.n_pages) * 4);
 }
 
 int launch_pages_extend(const tq_pages& in, const tq_pages& out, int64_t n, const int32_t* seqs,
@@ -489,7 +553,7 @@ int launch_pages_extend(const tq_pages& in, const tq_pages& out, int64_t n, cons
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool same = is_same(in, out);
   const int k = static_cast<int>(n);
-  if (int e = launch_dependent(k_plan_extend, plan_grid(in, same), dim3(kPlan), 0, st, in, out, k, seqs, new_tokens,
+  if (int e = launch_dependent(k_plan_extend, plan_grid(in, same, 0), dim3(kPlan), 0, st, in, out, k, seqs, new_tokens,
                                slots ? n_slots : -1, ws))
     return e;
   return launch_dependent(k_apply_extend, rows_grid(in), dim3(kRowThreads), 0, st, in, out, k, new_tokens, slots,
@@ -501,9 +565,10 @@ int launch_pages_fork(const tq_pages& in, const tq_pages& out, int64_t n, const 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool same = is_same(in, out);
   const int k = static_cast<int>(n);
-  if (int e = launch_dependent(k_plan_fork, plan_grid(in, same), dim3(kPlan), 0, st, in, out, k, src, dst, moves, ws))
-    return e;
-  return launch_dependent(k_apply_fork, rows_grid(in), dim3(kRowThreads), 0, st, in, out, k, src, same, ws);
+  const dim3 plan = plan_grid(in, same, n);
+  if (int e = launch_dependent(k_plan_fork, plan, dim3(kPlan), 0, st, in, out, k, src, dst, moves, ws)) return e;
+  return launch_dependent(k_apply_fork, rows_grid(in), dim3(kRowThreads), 0, st, in, out, k, src, moves,
+                          static_cast<int>(plan.x - 1), same, ws);
 }
 
 int launch_pages_free(const tq_pages& in, const tq_pages& out, int64_t n, const int32_t* seqs, void* ws,
@@ -511,17 +576,20 @@ int launch_pages_free(const tq_pages& in, const tq_pages& out, int64_t n, const 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool same = is_same(in, out);
   const int k = static_cast<int>(n);
-  if (int e = launch_dependent(k_plan_free, plan_grid(in, same), dim3(kPlan), 0, st, in, out, k, seqs, ws)) return e;
-  return launch_dependent(k_apply_free, rows_grid(in), dim3(kRowThreads), 0, st, in, out, k, same, ws);
+  const dim3 plan = plan_grid(in, same, n);
+  if (int e = launch_dependent(k_plan_free, plan, dim3(kPlan), 0, st, in, out, k, seqs, ws)) return e;
+  return launch_dependent(k_apply_free, rows_grid(in), dim3(kRowThreads), 0, st, in, out, k,
+                          static_cast<int>(plan.x - 1), same, ws);
 }
 
 int launch_pages_compact(const tq_pages& in, const tq_pages& out, int32_t* moves, void* ws, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool same = is_same(in, out);
-  if (int e = launch_dependent(k_plan_compact, plan_grid(in, same), dim3(kPlan), 0, st, in, out, moves,
-                               std::max<int64_t>(1, in.n_pages / 2), ws))
-    return e;
-  return launch_dependent(k_apply_compact, rows_grid(in), dim3(kRowThreads), 0, st, in, out, moves, same, ws);
+  const dim3 plan = plan_grid(in, same, in.n_seqs);
+  const int64_t most = std::max<int64_t>(1, in.n_pages / 2);
+  if (int e = launch_dependent(k_plan_compact, plan, dim3(kPlan), 0, st, in, out, moves, most, ws)) return e;
+  return launch_dependent(k_apply_compact, rows_grid(in), dim3(kRowThreads), 0, st, in, out, moves, most,
+                          static_cast<int>(plan.x - 1), same, ws);
 }
 
 int launch_pages_copy(void* base, int64_t n_layers, int64_t layer_stride, int64_t page_bytes, int64_t n_pages,

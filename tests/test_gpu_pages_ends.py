@@ -83,3 +83,43 @@ def test_no_room_for_slots_is_no_room(tq):
     unchanged(tq, T, before, None, lambda: T.extend(i32([3, 0]), i32([0, 1]), 0))
     T.extend(i32([3, 0]), i32([0, 0]), 0)
     T.check()
+
+
+@pytest.mark.parametrize("into", [False, True])
+@pytest.mark.parametrize("at,entry", [(0, -1), (0, 12), (1, 1 << 30), (0, "free"), (2, -7), (2, 12), (2, "free")])
+def test_bad_entries_leave_all_as_it_was(tq, into, at, entry):
+    """A row whose entry is no page, or a page that nobody owns: none of the
+    calls that go by the row does part of its work."""
+    T = tq.PageTable.empty(6, 4, 12, 16)
+    T.extend(i32([1, 0, 2, 4]), i32([30, 40, 17, 5]), 92)        # row 0: two full pages and a tail
+    T.free(i32([1]))                                             # a hole, so that compaction moves
+    T.check()
+    T.table[0, at] = int(torch.nonzero(T.refs == 0)[-1]) if entry == "free" else entry
+    before = arrays(T)
+    out = other(tq, T) if into else None
+    m = unchanged(tq, T, before, out, lambda: T.fork(i32([2, 0]), i32([3, 5]), out=out))
+    assert torch.all(m.pairs == -1)
+    unchanged(tq, T, before, out, lambda: T.free(i32([2, 0, 2]), out=out))
+    m = unchanged(tq, T, before, out, lambda: T.compact(out=out))
+    assert torch.all(m.pairs == -1)
+    # calls that do not go by the row are done
+    m = T.fork(i32([2]), i32([3]), out=out)
+    T.check()
+    assert (out or T).lens.tolist() == [40, 0, 17, 17, 5, 0] and int((m.pairs >= 0).sum()) == 2
+
+
+def test_bad_entries_of_many_rows(tq):
+    """One bad entry in a table of rows for many CTAs, whichever row has it."""
+    n = 9000
+    T = tq.PageTable.empty(n, 3, 3 * n, 16)
+    T.extend(i32(range(n)), i32([33] * n), 33 * n)
+    T.check()
+    for row in (0, 31, 4567, n - 1):
+        T.table[row, 1] = -3
+        before = arrays(T)
+        unchanged(tq, T, before, None, lambda: T.free(i32(range(n))))
+        unchanged(tq, T, before, None, lambda: T.compact())
+        T.table[row, 1] = before[0][row, 0] + 1
+    T.free(i32(range(n)))
+    T.check()
+    assert not T.refs.any() and torch.all(T.table == -1)
