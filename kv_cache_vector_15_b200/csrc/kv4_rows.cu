@@ -17,7 +17,8 @@
 // quotient is further from a border than its error: (x - z), 1 / (15 s), their
 // product and its product with 15 are each off by at most 2^-24 of at most 16,
 // 4e-6 in all, so a thread that has a quotient within 1e-5 of a border
-// compares in fp64, in which (x - z) and (k + 1/2) s are exact.  Otherwise the
+// compares x with the border z + (k + 1/2) s in fp64, in which that is exact
+// (x - z is not, for an x far smaller than z).  Otherwise the
 // clamp to [0, 15] is the product's saturation, and the rounding an addition
 // of 1.5 * 2^23 whose low bits are the code: 7 instructions a coordinate.
 #include <cuda_bf16.h>
@@ -202,9 +203,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 6 : 5) k_kv4_append
         const float f15 = __saturatef((x[i] - zero) * inv) * 15.f, f = floorf(fminf(f15, 14.9f));
         float r = rintf(f15);
         if (fabsf(f15 - f - 0.5f) < 2e-5f) {
-          const double diff = (static_cast<double>(x[i]) - static_cast<double>(zero)) -
-                              (static_cast<double>(f) + 0.5) * static_cast<double>(s);
-          r = diff > 0.0 ? f + 1.f : diff < 0.0 ? f : 2.f * rintf(0.5f * f + 0.25f);   // a tie: the even one
+          const double border = (static_cast<double>(f) + 0.5) * static_cast<double>(s) + static_cast<double>(zero);
+          const double at = static_cast<double>(x[i]);
+          r = at > border ? f + 1.f : at < border ? f : 2.f * rintf(0.5f * f + 0.25f);   // a tie: the even one
         }
         q[i] = r;
         codes[i / 8] |= static_cast<uint32_t>(r) << (4 * (i & 7));

@@ -27,9 +27,13 @@ def quantize(x):
     for pair in (scale, zero):
         pair.view(np.uint16)[np.isnan(g).any(-1)] = 0x7fff
     s, z = scale.astype(np.float64)[..., None], zero.astype(np.float64)[..., None]
-    with np.errstate(divide="ignore", invalid="ignore"):
-        t = np.where(s > 0, (g.astype(np.float64) - z) / s, 0.0)
-    return np.clip(np.rint(t), 0, 15).astype(np.int64).reshape(x.shape), scale, zero
+    # the exact quotient, to the nearest: a code per border z + (k + 1/2) s (exact in fp64) that x lies behind; on the
+    # border itself the even one of the two codes
+    x64, codes = g.astype(np.float64), np.zeros(g.shape, np.int64)
+    for k in range(15):
+        border = z + (k + 0.5) * s
+        codes += (s > 0) & ((x64 > border) | ((x64 == border) & (k % 2 == 1)))
+    return codes.reshape(x.shape), scale, zero
 
 
 def values(codes, scale, zero):

@@ -183,3 +183,23 @@ def test_nan_rows_stay_nan(tq, dtype):
             for h in range(H):
                 o.write_slot(want, int(slots[t]), part, h, c[t, h], s[t, h], z[t, h], H, d, ps)
     assert np.array_equal(C.pool.cpu().numpy(), want)
+
+
+def test_quotients_that_64_bits_do_not_tell_from_a_border(tq):
+    """x a little beside zero, zero a border between two codes: x - z is the
+    border itself in 64 bits, the exact quotient is not."""
+    C = tq.KV4Cache.empty(15, 1, 64, 16)
+    tiny = np.float32([2.0 ** -60, 2.0 ** -149, 1e-30, 0.0, -0.0, -1e-30, -2.0 ** -149, -2.0 ** -60])
+    x = np.empty((15, 1, 64), np.float32)
+    want = np.empty((15, 64))
+    for k in range(15):
+        z = -(2.0 * k + 1)                                       # s = 2: zero is the border behind code k
+        x[k, 0] = np.concatenate([[z, z + 30], np.resize(tiny, 62)])
+        up = x[k, 0] > 0
+        want[k] = z + 2 * np.where(up, k + 1, k)
+        want[k][x[k, 0] == 0] = z + 2 * (k + k % 2)              # a tie: the even code
+        want[k, :2] = z, z + 30
+    got, _ = C.append(dev(x), dev(x), torch.arange(15, device="cuda"), return_values=True)
+    assert np.array_equal(got.double().cpu().numpy()[:, 0], want)
+    c, s, z = o.quantize(x)
+    assert np.array_equal(o.values(c, s, z)[:, 0], want)
