@@ -313,24 +313,24 @@ PyObject* kv4_attention(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
 }
 
 // Lists of sequences: int32, contiguous, of one length.
-int64_t lists(const Place& at, const at::Tensor& table, const at::Tensor& x, const at::Tensor& y = {}) {
-  at.all(table, x, y);
+int64_t lists(const Place& at, const at::Tensor& x, const at::Tensor& y = {}) {
+  at.all(x, y);
   const int64_t n = x.numel();
   want(x, at::kInt, {n}, "an index list");
   want(y, at::kInt, {n}, "an index list");
   return n;
 }
 
-// in, out, table, seqs, new_tokens, n_slots, workspace, stream
+// in, out, in's table, out's, seqs, new_tokens, n_slots, workspace, stream
 PyObject* pages_extend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    count(n_args, 8);
+    count(n_args, 9);
     const tq_pages &in = *address<tq_pages>(a[0]), &out = *address<tq_pages>(a[1]);
-    const at::Tensor table = tensor(a[2], "table"), seqs = tensor(a[3], "seqs"), more = tensor(a[4], "new_tokens");
-    const at::Tensor given = tensor(a[6], "workspace", false);
-    Place at(a[7]);
-    const int64_t n = lists(at, table, seqs, more), n_slots = integer(a[5]);
-    at.on(given);
+    const at::Tensor table = tensor(a[2], "table"), into = tensor(a[3], "out.table");
+    const at::Tensor seqs = tensor(a[4], "seqs"), more = tensor(a[5], "new_tokens"), given = tensor(a[7], "workspace", false);
+    Place at(a[8]);
+    at.all(table, into, given);
+    const int64_t n = lists(at, seqs, more), n_slots = integer(a[6]);
     if (n_slots < 0) throw ValueError("n_slots must be >= 0");
     std::optional<NoGil> free(std::in_place);
     // a list of no slots has an address too: without one the call would take it that no list is wanted
@@ -345,17 +345,17 @@ PyObject* pages_extend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// in, out, table, src, dst, moves, workspace, stream
+// in, out, in's table, out's, src, dst, moves, workspace, stream
 PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    count(n_args, 8);
+    count(n_args, 9);
     const tq_pages &in = *address<tq_pages>(a[0]), &out = *address<tq_pages>(a[1]);
-    const at::Tensor table = tensor(a[2], "table"), src = tensor(a[3], "src"), dst = tensor(a[4], "dst");
-    const at::Tensor given = tensor(a[6], "workspace", false);
-    at::Tensor moves = tensor(a[5], "moves", false);
-    Place at(a[7]);
-    const int64_t n = lists(at, table, src, dst);
-    at.all(given, moves);
+    const at::Tensor table = tensor(a[2], "table"), into = tensor(a[3], "out.table");
+    const at::Tensor src = tensor(a[4], "src"), dst = tensor(a[5], "dst"), given = tensor(a[7], "workspace", false);
+    at::Tensor moves = tensor(a[6], "moves", false);
+    Place at(a[8]);
+    at.all(table, into, given, moves);
+    const int64_t n = lists(at, src, dst);
     want(moves, at::kInt, {n, 2}, "moves");
     std::optional<NoGil> free(std::in_place);
     if (!moves.defined()) moves = at.output(make(table, {n, 2}));
@@ -368,15 +368,16 @@ PyObject* pages_fork(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// in, out, table, seqs, workspace, stream
+// in, out, in's table, out's, seqs, workspace, stream
 PyObject* pages_free(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    count(n_args, 6);
+    count(n_args, 7);
     const tq_pages &in = *address<tq_pages>(a[0]), &out = *address<tq_pages>(a[1]);
-    const at::Tensor table = tensor(a[2], "table"), seqs = tensor(a[3], "seqs"), given = tensor(a[4], "workspace", false);
-    Place at(a[5]);
-    const int64_t n = lists(at, table, seqs);
-    at.on(given);
+    const at::Tensor table = tensor(a[2], "table"), into = tensor(a[3], "out.table");
+    const at::Tensor seqs = tensor(a[4], "seqs"), given = tensor(a[5], "workspace", false);
+    Place at(a[6]);
+    at.all(table, into, given);
+    const int64_t n = lists(at, seqs);
     std::optional<NoGil> free(std::in_place);
     size_t bytes = 0;
     const at::Tensor ws = workspace(given, tqlib.pages_workspace_bytes(in, n), table, &bytes);
@@ -387,15 +388,15 @@ PyObject* pages_free(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
-// in, out, table, moves, workspace, stream
+// in, out, in's table, out's, moves, workspace, stream
 PyObject* pages_compact(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   return guarded([&]() -> PyObject* {
-    count(n_args, 6);
+    count(n_args, 7);
     const tq_pages &in = *address<tq_pages>(a[0]), &out = *address<tq_pages>(a[1]);
-    const at::Tensor table = tensor(a[2], "table"), given = tensor(a[4], "workspace", false);
-    at::Tensor moves = tensor(a[3], "moves", false);
-    Place at(a[5]);
-    at.all(table, given, moves);
+    const at::Tensor table = tensor(a[2], "table"), into = tensor(a[3], "out.table"), given = tensor(a[5], "workspace", false);
+    at::Tensor moves = tensor(a[4], "moves", false);
+    Place at(a[6]);
+    at.all(table, into, given, moves);
     const int64_t most = std::max<int64_t>(1, in.n_pages / 2);
     want(moves, at::kInt, {most, 2}, "moves");
     std::optional<NoGil> free(std::in_place);

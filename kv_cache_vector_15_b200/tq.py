@@ -646,21 +646,25 @@ class PageTable:
     def extend(self, seqs, new_tokens, n_slots: int, out=None, workspace=None, stream=None):
         """Room for new_tokens[i] more tokens of sequence seqs[i] (int32 [n]
         each); returns the slots of the new tokens (int64 [n_slots], -1 behind the last)."""
-        return (_calls or _load_calls()).pages_extend(self._at, (out or self)._at, self.table, seqs, new_tokens, n_slots,
+        out = out or self
+        return (_calls or _load_calls()).pages_extend(self._at, out._at, self.table, out.table, seqs, new_tokens, n_slots,
                                                       workspace, stream)
 
     def fork(self, src, dst, out=None, moves=None, workspace=None, stream=None) -> PageMoves:
         """Sequence dst[i] (empty) becomes a copy of src[i]; the moves are still to be copied."""
-        return PageMoves((_calls or _load_calls()).pages_fork(self._at, (out or self)._at, self.table, src, dst, moves,
+        out = out or self
+        return PageMoves((_calls or _load_calls()).pages_fork(self._at, out._at, self.table, out.table, src, dst, moves,
                                                               workspace, stream), self.n_pages)
 
     def free(self, seqs, out=None, workspace=None, stream=None):
         """Sequences ``seqs`` (int32 [n]) end."""
-        (_calls or _load_calls()).pages_free(self._at, (out or self)._at, self.table, seqs, workspace, stream)
+        out = out or self
+        (_calls or _load_calls()).pages_free(self._at, out._at, self.table, out.table, seqs, workspace, stream)
 
     def compact(self, out=None, moves=None, workspace=None, stream=None) -> PageMoves:
         """The used pages move to the front; the moves are still to be copied."""
-        return PageMoves((_calls or _load_calls()).pages_compact(self._at, (out or self)._at, self.table, moves, workspace,
+        out = out or self
+        return PageMoves((_calls or _load_calls()).pages_compact(self._at, out._at, self.table, out.table, moves, workspace,
                                                                  stream), self.n_pages)
 
 

@@ -123,3 +123,21 @@ def test_bad_entries_of_many_rows(tq):
     T.free(i32(range(n)))
     T.check()
     assert not T.refs.any() and torch.all(T.table == -1)
+
+
+def test_tables_of_another_device(tq):
+    """Where out's arrays are is checked as in's are (here: on the host; the addresses are T's own)."""
+    T = tq.PageTable.empty(4, 4, 10, 16)
+    T.extend(i32([0]), i32([20]), 20)
+    T.check()
+    before, launches = arrays(T), tq.launch_count()
+
+    class Far:
+        table, _at = T.table.cpu(), T._at
+
+    for call in (lambda: T.extend(i32([0]), i32([1]), 1, out=Far), lambda: T.fork(i32([0]), i32([1]), out=Far),
+                 lambda: T.free(i32([0]), out=Far), lambda: T.compact(out=Far)):
+        with pytest.raises(ValueError, match="cpu"):
+            call()
+    assert tq.launch_count() == launches
+    assert all(torch.equal(x, y) for x, y in zip(before, arrays(T)))
