@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import operator
 import os
 from dataclasses import dataclass
 
@@ -460,20 +461,30 @@ class TurboQuantSplit:
         return out
 
 
+def _fixed(*names):
+    """Attributes that cannot be set anew: their arrays' addresses are held beside them."""
+    def add(cls):
+        for name in names:
+            setattr(cls, name, property(operator.attrgetter("_" + name)))
+        return cls
+    return add
+
+
+@_fixed("inv_freq", "axis", "interleaved", "rot_dim")
 class Rope:
     """A rotary position plan for qk_norm_rope: inv_freq [rot_dim / 2] (host
     numbers), pairs (i, i + rot_dim / 2) or, interleaved, (2 i, 2 i + 1); axis
     [rot_dim / 2]: which row of the positions turns pair i (None: the only one)."""
 
     def __init__(self, inv_freq, interleaved: bool = False, axis=None):
-        self.inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64).reshape(-1)
-        self.axis = None if axis is None else np.ascontiguousarray(axis, dtype=np.int32).reshape(-1)
-        if self.axis is not None and self.axis.shape != self.inv_freq.shape:
+        self._inv_freq = np.array(inv_freq, dtype=np.float64, order="C").reshape(-1)          # its own numbers, not the caller's array
+        self._axis = None if axis is None else np.array(axis, dtype=np.int32, order="C").reshape(-1)
+        if self._axis is not None and self._axis.shape != self._inv_freq.shape:
             raise ValueError("axis and inv_freq differ in length")
-        self.interleaved = bool(interleaved)
-        self.rot_dim = 2 * self.inv_freq.size
-        self._c = (self.rot_dim, int(self.interleaved), self.inv_freq.ctypes.data,
-                   0 if self.axis is None else self.axis.ctypes.data)
+        self._interleaved = bool(interleaved)
+        self._rot_dim = 2 * self._inv_freq.size
+        self._c = (self._rot_dim, int(self._interleaved), self._inv_freq.ctypes.data,
+                   0 if self._axis is None else self._axis.ctypes.data)
 
     def __reduce__(self):                      # copies hold addresses of their own arrays
         return Rope, (self.inv_freq.copy(), self.interleaved, None if self.axis is None else self.axis.copy())
@@ -530,6 +541,7 @@ def kv4_page_bytes(d: int, kv_heads: int, page_size: int) -> int:
     return n
 
 
+@_fixed("pool", "status", "kv_heads", "d", "page_size")
 class KV4Cache:
     """One layer's keys and values in paged 4-bit form: ``pool`` is uint8
     [n_pages, kv4_page_bytes(d, kv_heads, page_size)] on the current CUDA device."""
@@ -538,9 +550,9 @@ class KV4Cache:
         import torch
         _on_device(pool)
         _want(pool, torch.uint8, (pool.shape[0], kv4_page_bytes(d, kv_heads, page_size)), "pool")
-        self.pool, self.kv_heads, self.d, self.page_size = pool, kv_heads, d, page_size
-        self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
-        self._c = _KV4(pool.data_ptr(), pool.shape[0], d, kv_heads, page_size, self.status.data_ptr())
+        self._pool, self._kv_heads, self._d, self._page_size = pool, kv_heads, d, page_size
+        self._status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self._c = _KV4(pool.data_ptr(), pool.shape[0], d, kv_heads, page_size, self._status.data_ptr())
         self._at = ctypes.addressof(self._c)
 
     @staticmethod
@@ -557,7 +569,7 @@ class KV4Cache:
         """Write rows k, v [n, kv_heads, d] (bf16 or fp32) into ``slots`` (int64
         [n], negative: skipped); with return_values, what the stored codes
         stand for, in the rows' dtype."""
-        return (_calls or _load_calls()).kv4_append(self._at, self.pool, k, v, slots, return_values, stream)
+        return (_calls or _load_calls()).kv4_append(self._at, self._pool, k, v, slots, return_values, stream)
 
     def dequant(self, slots, out_dtype=None, k=None, v=None, stream=None):
         """The rows at ``slots`` as (k, v) [n, kv_heads, d]; rows of negative slots are left as they were."""
@@ -588,7 +600,7 @@ class KV4Cache:
         defaults to 1/sqrt(d).  Returns out (q's shape and dtype), or (out,
         lse [n_tokens, q_heads] fp32); rows behind cu_q[-1] are not written
         (in new tensors they hold anything)."""
-        return (_calls or _load_calls()).kv4_attention(self._at, self.pool, q, page_table, seq_lens, cu_q, max_q, scale,
+        return (_calls or _load_calls()).kv4_attention(self._at, self._pool, q, page_table, seq_lens, cu_q, max_q, scale,
                                                        causal, window, out, lse, return_lse, workspace, stream)
 
 
@@ -613,6 +625,7 @@ def copy_pages(pool, pairs, n_pages: int, stream=None, n_layers: int | None = No
     (_calls or _load_calls()).copy_pages(pool, pairs, n_pages, n_layers, stream)
 
 
+@_fixed("table", "lens", "refs", "status", "page_size", "n_pages")
 class PageTable:
     """Which pages a cache's sequences own: table int32 [n_seqs, max_pages],
     lens int32 [n_seqs], refs int32 [n_pages], on the current CUDA device.
@@ -625,11 +638,11 @@ class PageTable:
         _want(table, torch.int32, (lens.numel(), table.shape[1]), "table")
         _want(lens, torch.int32, (lens.numel(),), "lens")
         _want(refs, torch.int32, (refs.numel(),), "refs")
-        self.table, self.lens, self.refs, self.page_size = table, lens, refs, page_size
-        self.status = torch.zeros(1, dtype=torch.int32, device=table.device)
-        self.n_pages = refs.numel()
+        self._table, self._lens, self._refs, self._page_size = table, lens, refs, page_size
+        self._status = torch.zeros(1, dtype=torch.int32, device=table.device)
+        self._n_pages = refs.numel()
         self._c = _Pages(table.data_ptr(), lens.data_ptr(), refs.data_ptr(), lens.numel(), table.shape[1],
-                         self.n_pages, page_size, self.status.data_ptr())
+                         self._n_pages, page_size, self._status.data_ptr())
         self._at = ctypes.addressof(self._c)
 
     @staticmethod
@@ -647,24 +660,24 @@ class PageTable:
         """Room for new_tokens[i] more tokens of sequence seqs[i] (int32 [n]
         each); returns the slots of the new tokens (int64 [n_slots], -1 behind the last)."""
         out = out or self
-        return (_calls or _load_calls()).pages_extend(self._at, out._at, self.table, out.table, seqs, new_tokens, n_slots,
+        return (_calls or _load_calls()).pages_extend(self._at, out._at, self._table, out.table, seqs, new_tokens, n_slots,
                                                       workspace, stream)
 
     def fork(self, src, dst, out=None, moves=None, workspace=None, stream=None) -> PageMoves:
         """Sequence dst[i] (empty) becomes a copy of src[i]; the moves are still to be copied."""
         out = out or self
-        return PageMoves((_calls or _load_calls()).pages_fork(self._at, out._at, self.table, out.table, src, dst, moves,
+        return PageMoves((_calls or _load_calls()).pages_fork(self._at, out._at, self._table, out.table, src, dst, moves,
                                                               workspace, stream), self.n_pages)
 
     def free(self, seqs, out=None, workspace=None, stream=None):
         """Sequences ``seqs`` (int32 [n]) end."""
         out = out or self
-        (_calls or _load_calls()).pages_free(self._at, out._at, self.table, out.table, seqs, workspace, stream)
+        (_calls or _load_calls()).pages_free(self._at, out._at, self._table, out.table, seqs, workspace, stream)
 
     def compact(self, out=None, moves=None, workspace=None, stream=None) -> PageMoves:
         """The used pages move to the front; the moves are still to be copied."""
         out = out or self
-        return PageMoves((_calls or _load_calls()).pages_compact(self._at, out._at, self.table, out.table, moves, workspace,
+        return PageMoves((_calls or _load_calls()).pages_compact(self._at, out._at, self._table, out.table, moves, workspace,
                                                                  stream), self.n_pages)
 
 

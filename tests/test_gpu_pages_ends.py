@@ -141,3 +141,13 @@ def test_tables_of_another_device(tq):
             call()
     assert tq.launch_count() == launches
     assert all(torch.equal(x, y) for x, y in zip(before, arrays(T)))
+
+
+def test_arrays_cannot_be_replaced(tq):
+    """A table or cache holds its arrays' addresses: others cannot be put in their place."""
+    T, C = tq.PageTable.empty(2, 2, 4, 16), tq.KV4Cache.empty(2, 1, 64, 16)
+    for x, names in ((T, ("table", "lens", "refs", "status", "page_size", "n_pages")),
+                     (C, ("pool", "status", "kv_heads", "d", "page_size"))):
+        for name in names:
+            with pytest.raises(AttributeError):
+                setattr(x, name, getattr(x, name))
