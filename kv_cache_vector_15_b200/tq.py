@@ -577,9 +577,14 @@ class KV4Cache:
         _on_device(self.pool, slots, k, v)
         _want(slots, torch.int64, (slots.numel(),), "slots")
         shape, dt = (slots.numel(), self.kv_heads, self.d), out_dtype or (k.dtype if k is not None else torch.bfloat16)
+        new = [x is None for x in (k, v)]
         with torch.cuda.stream(None if stream is None else torch.cuda.ExternalStream(stream.cuda_stream)):
             k = torch.zeros(shape, dtype=dt, device=slots.device) if k is None else k
             v = torch.zeros(shape, dtype=dt, device=slots.device) if v is None else v
+        if stream is not None:                                # new ones belong to it, and are used on the current stream
+            for x, made in zip((k, v), new):
+                if made:
+                    x.record_stream(torch.cuda.current_stream())
         _want(k, dt, shape, "k")
         _want(v, dt, shape, "v")
         _check(_lib.tq_kv4_dequant(self._c, _ptr(slots), shape[0], _ptr(k), _ptr(v), _dtype_code(k),

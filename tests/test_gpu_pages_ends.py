@@ -151,3 +151,23 @@ def test_arrays_cannot_be_replaced(tq):
         for name in names:
             with pytest.raises(AttributeError):
                 setattr(x, name, getattr(x, name))
+
+
+def test_outputs_of_dequant_on_another_stream(tq):
+    """What a call on a given stream returns may go while the calling stream still reads it."""
+    C = tq.KV4Cache.empty(64, 8, 128, 16)
+    x = torch.randn((1024, 8, 128), device="cuda")
+    slots = torch.arange(1024, device="cuda")
+    C.append(x, x, slots)
+    want = C.dequant(slots)[0]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    k, v = C.dequant(slots, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(100_000_000)
+    got = k.clone()                                              # behind the pause
+    del k, v
+    with torch.cuda.stream(side):
+        junk = [torch.full_like(want, float("nan")) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(junk) == 4
