@@ -15,6 +15,7 @@ using namespace tq;
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 tq_status cuda_fail(int err, const char* what) {
+  cudaGetLastError();                          // the thread's last error goes with the report
   return fail(TQ_ERR_CUDA, std::string(what) + ": " + cuda_error_string(err));
 }
 

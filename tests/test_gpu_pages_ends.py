@@ -171,3 +171,24 @@ def test_outputs_of_dequant_on_another_stream(tq):
         junk = [torch.full_like(want, float("nan")) for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and len(junk) == 4
+
+
+def test_errors_of_the_runtime_do_not_stay(tq):
+    """A call that the CUDA runtime refuses reports it, and the thread's last
+    error is not left to whoever asks next.  (The status call waits for its
+    stream, which a stream under capture does not allow.)"""
+    import ctypes
+    rt = ctypes.CDLL("libcudart.so.12")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    s, g = ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreateWithFlags(ctypes.byref(s), 1) == 0
+    assert rt.cudaStreamBeginCapture(s, 2) == 0                  # relaxed: other calls of the process go on
+    st = tq.call_status("tq_cache_status", word.data_ptr(), s)
+    left = rt.cudaPeekAtLastError()
+    rt.cudaStreamEndCapture(s, ctypes.byref(g))
+    rt.cudaGetLastError()
+    if g.value:
+        rt.cudaGraphDestroy(g)
+    assert rt.cudaStreamDestroy(s) == 0
+    assert st == tq.TQ_ERR_CUDA and left == 0
