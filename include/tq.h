@@ -464,8 +464,8 @@ size_t tq_pages_workspace_bytes(tq_pages pages, int64_t n);
 /* Room for new_tokens[i] (>= 0) more tokens of sequence seqs[i] (device int32
  * [n], distinct): takes free pages, counts lens up, and writes the new tokens'
  * slots (page * page_size + place), sequence after sequence in the order of
- * `seqs`, to slots (device int64 [n_slots], -1 behind the last; NULL: not
- * wanted; more tokens than n_slots is an error). */
+ * `seqs`, to slots (device int64 [n_slots], n_slots < 2^31, -1 behind the last;
+ * NULL: not wanted; more tokens than n_slots is an error). */
 tq_status tq_pages_extend(tq_pages in, tq_pages out, int64_t n, const int32_t* seqs, const int32_t* new_tokens,
                           int64_t* slots, int64_t n_slots, void* workspace, size_t workspace_bytes, void* stream);
 

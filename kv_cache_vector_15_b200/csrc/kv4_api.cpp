@@ -237,7 +237,8 @@ tq_status tq_pages_extend(tq_pages in, tq_pages out, int64_t n, const int32_t* s
   if (st != TQ_OK) return st;
   if (n && (!seqs || !new_tokens || !aligned(seqs, 4) || !aligned(new_tokens, 4)))
     return fail(TQ_ERR_INVALID_ARG, "seqs and new_tokens must be given, 4-byte aligned");
-  if (n_slots < 0 || !aligned(slots, 8)) return fail(TQ_ERR_INVALID_ARG, "n_slots < 0, or slots not 8-byte aligned");
+  if (n_slots < 0 || n_slots > INT32_MAX || !aligned(slots, 8))   // the new tokens' places in the list are 32-bit numbers
+    return fail(TQ_ERR_INVALID_ARG, "n_slots must be in [0, 2^31), slots 8-byte aligned");
   const int err = launch_pages_extend(in, out, n, seqs, new_tokens, slots, n_slots, workspace, stream);
   return err ? cuda_fail(err, "tq_pages_extend launch") : TQ_OK;
 }

@@ -331,7 +331,7 @@ PyObject* pages_extend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     Place at(a[8]);
     at.all(table, into, given);
     const int64_t n = lists(at, seqs, more), n_slots = integer(a[6]);
-    if (n_slots < 0) throw ValueError("n_slots must be >= 0");
+    if (n_slots < 0 || n_slots > INT32_MAX) throw ValueError("n_slots must be in [0, 2^31)");
     std::optional<NoGil> free(std::in_place);
     // a list of no slots has an address too: without one the call would take it that no list is wanted
     at::Tensor slots = at.output(make(table, {std::max<int64_t>(1, n_slots)}, at::kLong));
