@@ -22,6 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libtq.so")
 CALLS_SRC = os.path.join(CSRC, "python", "calls.cpp")
 CALLS = os.path.join(HERE, "_calls.so")
+CALLS_FOR = os.path.join(BUILD, "calls.for")   # the interpreter and the torch that it was built for
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include"),
           "-I", CSRC]
@@ -57,13 +58,24 @@ def _compile(src: str, verbose: bool, force: bool = False) -> str:
     return obj
 
 
-def build_calls() -> str:
-    """The Python module: g++ against this interpreter's and torch's headers."""
+def build_calls() -> str | None:
+    """The Python module: g++ against this interpreter's and torch's headers.
+    Without torch there is nothing to build it against, nor a caller of it:
+    None, and libtq.so serves its C ABI alone."""
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return None
     newest = max(os.path.getmtime(CALLS_SRC), os.path.getmtime(os.path.join(ROOT, "include", "tq.h")))
-    if os.path.exists(CALLS) and os.path.getmtime(CALLS) > newest:
+    made_for = f"{sys.version}\n{torch.__version__}\n{os.path.dirname(torch.__file__)}\n"
+    try:
+        with open(CALLS_FOR) as f:
+            same = f.read() == made_for
+    except OSError:
+        same = False
+    if same and os.path.exists(CALLS) and os.path.getmtime(CALLS) > newest:
         return CALLS
     at = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
@@ -77,6 +89,9 @@ def build_calls() -> str:
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(CALLS_FOR, "w") as f:
+        f.write(made_for)
     return CALLS
 
 
@@ -91,7 +106,8 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    build_calls()
+    if build_calls() is None:
+        sys.stderr.write("no torch here: _calls.so, which tq.py's paged cache needs, is not built\n")
     return LIB
 
 

@@ -34,3 +34,39 @@ def test_lists_of_slots_that_32_bits_do_not_count(tq):
         assert tq.call_status("tq_pages_extend", t, t, 1, at, at, at, n_slots, at, 1 << 20, 0) == tq.TQ_ERR_INVALID_ARG
         assert "n_slots" in tq.last_error()
     assert tq.launch_count() == before
+
+
+def test_build_without_torch():
+    """libtq needs nvcc alone: without torch the build goes on, less the module that is built against it."""
+    import subprocess
+    import sys
+    code = "import sys; sys.modules['torch'] = None\nfrom kv_cache_vector_15_b200 import build\nassert build.build_calls() is None\n"
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+
+
+def test_module_follows_torch_and_python(tmp_path, monkeypatch):
+    """_calls.so is built again for another torch or interpreter, and not otherwise."""
+    import types
+
+    import torch
+
+    from kv_cache_vector_15_b200 import build
+    made = []
+
+    def compiler(cmd, **kw):
+        made.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return types.SimpleNamespace(returncode=0)
+
+    monkeypatch.setattr(build, "CALLS", str(tmp_path / "_calls.so"))
+    monkeypatch.setattr(build, "CALLS_FOR", str(tmp_path / "calls.for"))
+    monkeypatch.setattr(build.subprocess, "run", compiler)
+    for count in (1, 1):
+        assert build.build_calls() == build.CALLS and len(made) == count
+    monkeypatch.setattr(torch, "__version__", "another")
+    for count in (2, 2):
+        assert build.build_calls() == build.CALLS and len(made) == count
+    monkeypatch.setattr(build.sys, "version", "another")
+    for count in (3, 3):
+        assert build.build_calls() == build.CALLS and len(made) == count
