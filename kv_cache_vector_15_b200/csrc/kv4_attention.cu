@@ -39,13 +39,14 @@
 // joins in order of the line (no atomics: the same inputs give the same bits).
 //
 // Measured, bf16, 8 kv heads of 4 query heads, d = 128: 8 x 131072 tokens
-// 0.311 ms = 3.88 TB/s (59 % of the copy rate; the copies alone take 0.19 ms);
-// 64 ragged sequences of 130 to 9000 tokens 64 us; one of 1000 11.9 us, the join
-// included.  The schedulers issue in 54 % of their cycles, with 3 warps each:
-// between, warps wait for their own last results, for the ALU pipe (half rate,
-// 50 % busy) or for instructions (the loop is 12 KB); 4 warps each need 128
+// 0.312 to 0.316 ms = 3.85 TB/s (59 % of the copy rate; the copies alone take 0.19 ms);
+// 64 ragged sequences of 130 to 9000 tokens 65 to 67 us; one of 1000 12.1 us, the
+// join included.  The schedulers issue in 54 % of their cycles, with 3 warps each,
+// of which 0.92 can go on: it is independent work that is short, not slots.
+// Warps wait for their own last results, for the ALU pipe (half rate,
+// 51 % busy) or for instructions (the loop is 12 KB); 4 warps each need 128
 // registers, spill, and take 0.341 ms.  One block a step 0.36, the next step's
-// logits beside this one's values no gain; a third stage in the rings 0.313.
+// logits beside this one's values no gain; a third stage in the rings 0.002 slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -66,8 +67,10 @@ using namespace sm100;
 constexpr int kWarps = 4;                      // per CTA; each an independent worker
 constexpr int kMaxWorkers = 148 * 16;
 constexpr int kMinTiles = 4;                   // a worker's least share of the line: two steps
-constexpr int kCost = 5;                       // what a unit costs besides its tiles (query rows, sums: about 9000
-                                               // clocks), in tiles of 1800
+// What a unit costs besides its tiles (query rows, sums: about 9000 clocks), in tiles of 1800.  With 2, 5 and 9: 64
+// sequences of 130 .. 9000 tokens 72.0, 64.5, 63.8 us, 256 of 100 .. 500 70.5, 67.2, 64.8, 16 of 1 .. 30000 60.8, 46.4,
+// 38.0, 8 of 131072 309.5, 312.2, 313.4.
+constexpr int kCost = 5;
 
 // Blocks that a warp takes at a time, and stages of as many blocks in its ring.
 __host__ __device__ constexpr int blocks_of(int d, int nt) { return d <= 128 && nt == 1 ? 2 : 1; }
@@ -75,7 +78,10 @@ __host__ __device__ constexpr int stages_of(int d, int nt) {
   return d == 64 ? 8 / blocks_of(d, nt) : d == 128 ? (nt == 1 ? 2 : 4) : 3;
 }
 // Column tiles of 4 rows that a unit has: as many as the largest sequence
-// brings, up to two (d = 256: one, whose accumulators fill the registers).
+// brings, up to two (d = 256: one, whose accumulators fill the registers).  One
+// and two, 16 sequences of 8192 tokens, 8 kv heads, d = 128: 4 rows 53.2 and 76.8
+// us, 8 rows 91 and 78, 16 rows 168 and 135 (a unit of two reads the cache once
+// for 8 rows); d = 64 with 16384 tokens: 62 and 95, 110 and 96, 207 and 184.
 constexpr int tiles_for(int d, int64_t rows) { return d == 256 || rows <= 4 ? 1 : 2; }
 __host__ __device__ constexpr int ctas_of(int d, int nt) { return d <= 128 ? (nt == 1 ? 3 : 2) : 2; }
 
@@ -703,7 +709,13 @@ int run_d(Params& P, int d, int rows, cudaStream_t st) {
 }  // namespace
 
 // bf16 rows go to the kernel for many rows from 17 rows per kv head on: below,
-// its tiles of 128 rows are mostly empty.
+// its tiles of 128 rows are mostly empty.  This kernel and that one, 16 sequences
+// of 8192 tokens, 8 kv heads, d = 128: 16 rows 135 and 182 us, 20 rows 191 and
+// 184, 64 rows 487 and 187; d = 64, 16384 tokens: 184 and 264, 275 and 264; d =
+// 256, 4 kv heads: 166 and 184, 203 and 186.  (Short caches cross later: 4
+// sequences of 1000 tokens, 20 rows 20.5 and 27.9 us, 64 rows 31 and 31.)  fp32
+// rows stay here whatever their number: that kernel's query operands have the
+// 11 bits of binary16.
 bool kv4_prefill_applies(int bf16, int64_t rows) { return bf16 && rows > 16; }
 
 size_t kv4_attention_ws_bytes(int d, int bf16, int64_t rows) {

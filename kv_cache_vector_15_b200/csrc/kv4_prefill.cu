@@ -40,8 +40,9 @@
 // last wave.
 //
 // Measured, bf16, 4 sequences of 171 to 512 new tokens behind 4099 to 8200, 8 kv
-// heads of 4 query heads, d = 128 (122 GFLOP): 0.216 ms = 565 TFLOP/s, 35 % of the
-// GEMM rate.  A tile of 256 rows and 128 keys takes 6500 clocks: 4000 of products
+// heads of 4 query heads, d = 128 (122 GFLOP): 0.207 to 0.225 ms = 540 to 590 TFLOP/s,
+// 34 to 37 % of the GEMM rate; the tensor pipe is active in 50 % of the cycles.  A tile of
+// 256 rows and 128 keys takes 6500 clocks: 4000 of products
 // (two passes over K; operands in shared memory at N = 128 use all of its
 // bandwidth), the rest waiting for K to be unpacked, weights and query rows.
 // Waiting for K before the first Q tile's values instead of behind them: 0.238 ms;
@@ -67,7 +68,9 @@ namespace {
 using namespace sm100;
 
 constexpr int kCtas = 148;
-constexpr int kCost = 3;                       // what a unit costs besides its tiles, in tiles
+// What a unit costs besides its tiles, in tiles.  With 1, 3 and 6: the case above 223, 218, 217 us, 16 sequences of 64
+// rows behind 1000 tokens 61.0, 58.4, 57.8, 64 of 10 .. 32 rows behind 130 .. 2000 152, 119, 126, one of 400 30.9, 31.0, 33.9.
+constexpr int kCost = 3;
 constexpr float kShift = 7.f;                  // p = 2^(logit - m + kShift)
 
 __host__ __device__ constexpr int q_tiles_of(int d) { return d == 256 ? 1 : 2; }

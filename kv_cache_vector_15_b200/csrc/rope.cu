@@ -13,9 +13,11 @@
 // (3 to 5 shuffles).  Half-split rotations whose rot / 2 is no multiple of 4
 // take one pair per lane and step (their loads cannot be wider).  Three rows of
 // a lane are loaded before the angles are formed.  8192 tokens of 32 + 8 heads,
-// d = 128, bf16 (168 MB): 35.5 us, 4.7 TB/s; a row's address worked out from the
+// d = 128, bf16 (168 MB): 36 to 37 us, 4.6 TB/s; a row's address worked out from the
 // kernel's arguments 38 us; one row ahead 51 us; with the cosines and the weights
-// apart and bank conflicts 61 us.  Issue slots bound it; the next token's rows
+// apart and bank conflicts 61 us.  Issue slots are taken in 69 % of the cycles, and
+// between warps wait at the block's barrier for the angles, and for shared memory;
+// the next token's rows
 // loaded under this one's (4 tokens a block) cost registers and occupancy: 43 us;
 // 4 blocks an SM instead of 5 39 us, 6 (spills) 38 us.
 #include <cuda_bf16.h>

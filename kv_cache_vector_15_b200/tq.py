@@ -601,7 +601,9 @@ class KV4Cache:
                   stream=None):
         """Attention of q [n_tokens, q_heads, d] over the cached tokens of
         n_seqs sequences: page_table int32 [n_seqs, max_pages], seq_lens int32
-        [n_seqs], cu_q int32 [n_seqs + 1] (None: one token each); scale
+        [n_seqs], cu_q int32 [n_seqs + 1] (None: one token each); max_q: the
+        largest number of new tokens of a sequence, which chooses the kernel (1
+        is right for a prompt too, and slow: 2.4 ms where 0.21 do); scale
         defaults to 1/sqrt(d).  Returns out (q's shape and dtype), or (out,
         lse [n_tokens, q_heads] fp32); rows behind cu_q[-1] are not written
         (in new tensors they hold anything)."""
