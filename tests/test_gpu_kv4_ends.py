@@ -203,3 +203,21 @@ def test_quotients_that_64_bits_do_not_tell_from_a_border(tq):
     assert np.array_equal(got.double().cpu().numpy()[:, 0], want)
     c, s, z = o.quantize(x)
     assert np.array_equal(o.values(c, s, z)[:, 0], want)
+
+
+@pytest.mark.parametrize("nq,dtype,n", [(1, "bf16", 5000), (3, "f32", 700), (5, "bf16", 90), (60, "bf16", 3000)])
+def test_outputs_in_the_place_of_the_queries(tq, nq, dtype, n):
+    """out may be q: a row's output is written behind all reads of its query,
+    by one worker, or by the join behind all workers."""
+    rng = np.random.default_rng(n)
+    lens, H, g, d = [n, 40, n // 3], 2, 4, 128
+    k, v = rng.standard_normal((2, sum(lens), H, d)).astype(np.float32)
+    C, table = filled(tq, rng, lens, k, v, 16)
+    q = dev(rng.standard_normal((3 * nq, H * g, d)).astype(np.float32)).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    cu = torch.arange(4, device="cuda", dtype=torch.int32) * nq
+    args = (table, dev(np.array(lens, np.int32)), cu, nq)
+    want = C.attention(q, *args)
+    for _ in range(5):
+        x = q.clone()
+        assert C.attention(x, *args, out=x) is not None and torch.equal(x, want)
+    C.check()
