@@ -400,6 +400,7 @@ size_t tq_kv4_attention_workspace_bytes(tq_kv4 cache, tq_dtype dtype, int q_head
  * over the cached rows j of kv head h / (q_heads / kv_heads) that the token sees.
  *   q, out [n_tokens, q_heads, d], q with token stride ld_q (elements, rows
  *   16-byte aligned), out contiguous, 16-byte aligned, both bf16 or both fp32;
+ *   out may be q where that is contiguous, and must not overlap it otherwise;
  *   lse [n_tokens, q_heads] fp32 or NULL.
  *   Sequence s has the tokens [cu_q[s], cu_q[s + 1]) (device int32
  *   [n_seqs + 1]; NULL: one token each, n_tokens = n_seqs) and seq_lens[s]
