@@ -418,7 +418,9 @@ size_t tq_kv4_attention_workspace_bytes(tq_kv4 cache, tq_dtype dtype, int q_head
  *   kernel (results hold for any value >= 1).
  * Query rows are taken to 2^-21 of their largest coordinate (fp32 rows: 2^-29),
  * their products with the codes are exact, softmax statistics and sums are
- * fp32, the weights of the values have 16 bits (24 for fp32 rows).  For bf16 rows with more than
+ * fp32, the weights of the values have 16 bits (24 for fp32 rows), and count for
+ * up to 31 scales of a group (8 for fp32 rows), so that a value near zero in a
+ * group of large ones is off by up to 2^-12 of the group's scale.  For bf16 rows with more than
  * 16 of them per kv head (max_q * q_heads / kv_heads) the cached values and the
  * weights enter the products in binary16.  A page outside [0, n_pages), a length
  * outside [0, min(ld_table * page_size, 2^30)] or a cu_q that decreases or leaves

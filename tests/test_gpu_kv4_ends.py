@@ -44,6 +44,20 @@ def spoil(C, table, seq, part, tokens, head, group):
         C.pool[page, pair:pair + 4] = torch.tensor([0xff, 0x7f] * 2, dtype=torch.uint8, device="cuda")
 
 
+def small_values(C, dtype, many, n):
+    """What that bound leaves out, for outputs that are small beside the values
+    of their group: the few-row kernel's codes enter as 16 + c and c - 31 (bf16
+    rows), so the 2^-17 that p s is off by counts for up to 31 s and not for
+    |c - 8| s; the many-row kernel's p, binary16 with 2^7 for the largest, is
+    off by 2^-25 where it is below 2^-14, 2^-32 of the largest for each key."""
+    H, d, ps = C.kv_heads, C.d, C.page_size
+    s, z = (np.stack([o.read_rows(C.pool.cpu().numpy(), np.arange(C.pool.shape[0]), C.pool.shape[0] * ps, 1, h, H, d, ps)[i]
+                      for h in range(H)]).astype(np.float64) for i in (1, 2))
+    if many:
+        return n * 2.0 ** -32 * np.nanmax(np.abs(z) + 15 * s)
+    return 31 * 2.0 ** -17 * np.nanmax(s) if dtype == "bf16" else 0.0
+
+
 def compare(tq, C, table, lens, nq, q, causal=True, window=0, max_q=None):
     """The call against the oracle: NaN where the oracle has NaN, the rest within the derived bounds."""
     cu = np.concatenate([[0], np.cumsum(nq)]).astype(np.int32)
@@ -56,6 +70,7 @@ def compare(tq, C, table, lens, nq, q, causal=True, window=0, max_q=None):
         ref = o.attention(q.double().cpu().numpy(), C.pool.cpu().numpy(), table.cpu().numpy(), lens, cu, C.kv_heads, C.page_size,
                           d ** -0.5, causal, window)
         tol, ltol = attention_tolerance(ref, max(lens), dtype, many, d)
+        tol = tol + small_values(C, dtype, many, max(lens))
     got, gl = out.double().cpu().numpy(), lse.double().cpu().numpy()
     nan, lnan = np.isnan(ref[0]), np.isnan(ref[1])
     assert np.array_equal(np.isnan(got), nan), (np.isnan(got).sum(), nan.sum())
