@@ -563,6 +563,7 @@ class KV4Cache:
 
     def check(self, stream=None):
         """Wait for the stream and raise what kernels recorded (slots, pages or lengths out of range)."""
+        _on_device(self._status)                                 # another device's stream would not be the one to wait for
         _check(_lib.tq_cache_status(_ptr(self.status), _stream(stream)), "tq_cache_status")
 
     def append(self, k, v, slots, return_values: bool = False, stream=None):
@@ -661,6 +662,7 @@ class PageTable:
 
     def check(self, stream=None):
         """Wait for the stream and raise what kernels recorded (a call that did nothing, and why)."""
+        _on_device(self._status)                                 # another device's stream would not be the one to wait for
         _check(_lib.tq_cache_status(_ptr(self.status), _stream(stream)), "tq_cache_status")
 
     def extend(self, seqs, new_tokens, n_slots: int, out=None, workspace=None, stream=None):

@@ -192,3 +192,13 @@ def test_errors_of_the_runtime_do_not_stay(tq):
         rt.cudaGraphDestroy(g)
     assert rt.cudaStreamDestroy(s) == 0
     assert st == tq.TQ_ERR_CUDA and left == 0
+
+
+def test_reports_of_another_device(tq):
+    """check() waits for a stream of the current device, so the status word has to be there (here it is on the host)."""
+    for cls in (tq.PageTable, tq.KV4Cache):
+        x = object.__new__(cls)
+        x._status = torch.ones(1, dtype=torch.int32)
+        with pytest.raises(ValueError, match="cpu"):
+            x.check()
+        assert int(x._status) == 1
